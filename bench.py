@@ -68,10 +68,14 @@ def act_bytes_per_elem(dtype):
     return _bytes_per_elem("bf16" if dtype == "bf16_mxfp8" else dtype)
 
 
+# sources of operators that the measured layer does not run and does not include
+OTHER_SOURCES = ("moe_fp8", "moe_balance")
+
+
 def kernel_source_hash():
-    """Hash of every kernel source (the counters describe one build)."""
+    """Hash of every kernel source of the layer (the counters describe one build)."""
     h = hashlib.sha256()
-    for name in sorted(os.listdir(CSRC)):
+    for name in sorted(n for n in os.listdir(CSRC) if not n.startswith(OTHER_SOURCES)):
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode() + f.read())
     return h.hexdigest()[:16]

@@ -314,6 +314,97 @@ MOE_API moe_status moe_nvfp4_linear_prepare(int32_t N, int32_t K, const void* co
 MOE_API moe_status moe_nvfp4_linear(int32_t M, int32_t N, int32_t K, const void* packed, const uint16_t* x,
                                     uint16_t* out, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---- Products on block-128 fp8 weights -------------------------------------
+ * Weights as e4m3fn codes [N, K] with one fp32 scale per 128 x 128 block,
+ * [ceil(N / 128), ceil(K / 128)] (weight = code * scale; the last blocks may be
+ * ragged), used as they are stored in checkpoints: nothing is repacked.
+ * Activations are bf16 rows, quantised inside per row and block of 128
+ * columns: amax = max(max |x|, 2^-100), scale = fp32(amax / 448), code =
+ * e4m3(fp32(x * fp32(448 / amax))), nearest, ties to even.  A row that holds
+ * an infinity or a NaN gives NaN in every column whose weights meet it.
+ * Sums are fp32.  On the fp8 matrix instruction a sum of a few thousand
+ * products carries a relative error of about 1.3e-5. */
+
+/* Quantise `count` stacked fp32 matrices [rows, K] into that form (a block's
+ * amax is over its 128 x 128 values).  K % 16 == 0, rows >= 1, both at most
+ * 2^20 (else MOE_ERR_UNSUPPORTED); w aligned to 16 bytes, codes to 4. */
+MOE_API moe_status moe_fp8_quantize_weights(int32_t count, int32_t rows, int32_t K, const float* w, void* codes,
+                                            float* scales, hipStream_t stream);
+
+/* Dense linear layer: out[m, n] = bf16( sum_k quant(x)[m, k] w[n, k] ).
+ * x bf16 [M, K] with rows x_stride elements apart (>= K, a multiple of 8), out
+ * bf16 [M, N] with rows out_stride elements apart (>= N); columns past N of an
+ * out row are left as they are.  Any N >= 1; K a multiple of 16; both at most
+ * 2^20 (else MOE_ERR_UNSUPPORTED); M <= 2^24, 0 is a no-op.  codes and x must
+ * be aligned to 16 bytes, ws to 256.  The gradient of x is the same product on
+ * the transposed codes and scales ([K, N]: 128 x 128 blocks transpose into
+ * blocks), with the output's gradient quantised per 128 of its columns.
+ * Workspace: moe_fp8_linear_workspace_bytes(max_M, N, K) bytes serve any M <=
+ * max_M (0 for unsupported arguments); its contents need not survive a call. */
+MOE_API size_t moe_fp8_linear_workspace_bytes(int32_t max_M, int32_t N, int32_t K);
+MOE_API moe_status moe_fp8_linear(int32_t M, int32_t N, int32_t K, const void* codes, const float* scales,
+                                  const uint16_t* x, int64_t x_stride, uint16_t* out, int64_t out_stride, void* ws,
+                                  size_t ws_bytes, hipStream_t stream);
+
+/* The expert MLPs of routed tokens on such weights: for sorted row r of expert
+ * e, p = sorted_pairs[r], t = p / top_k:
+ *   g, u = W13[e] . quant(x[t]) (rows [0, I) gate, [I, 2I) up; the shape's
+ *   gate_up_limit as in moe_gemm13_swiglu_quant), h = bf16(silu(g) * u),
+ *   y[p] = bf16( W2[e] . quant(h) ).
+ * offsets [E + 1] and sorted_pairs [T top_k] are moe_permute's outputs, x is
+ * bf16 [T, H], y bf16 [T top_k, H] (moe_combine's input): moe_route,
+ * moe_permute (with xq = x), moe_fp8_experts and moe_combine make the layer.
+ * w13 codes [E, 2I, H], scales [E, 2I / 128, H / 128]; w2 codes [E, H, I],
+ * scales [E, H / 128, I / 128].  shape: dtype MOE_BF16 (the activations'),
+ * activation MOE_SWIGLU, else MOE_ERR_UNSUPPORTED.  codes, x and y must be
+ * aligned to 16 bytes, ws (moe_fp8_experts_workspace_bytes(shape) bytes, 0 for
+ * an unsupported shape) to 256.  T == 0 is a no-op. */
+MOE_API size_t moe_fp8_experts_workspace_bytes(const moe_shape* shape);
+MOE_API moe_status moe_fp8_experts(const moe_shape* shape, int32_t T, const void* w13_codes, const float* w13_scales,
+                                   const void* w2_codes, const float* w2_scales, const int32_t* offsets,
+                                   const int32_t* sorted_pairs, const uint16_t* x, uint16_t* y, void* ws,
+                                   size_t ws_bytes, hipStream_t stream);
+
+/* ---- Training the router ----------------------------------------------------
+ * Losses of a batch of num_seqs sequences: sequence s holds the tokens
+ * [seq_offsets[s], seq_offsets[s + 1]) (device int32 [num_seqs + 1], ascending;
+ * NULL with num_seqs = 1: all T tokens), of which those with token_mask[t] != 0
+ * are valid (device u8 [T]; NULL: all).  With n_s valid tokens, c_{s,e} picks
+ * of expert e among them (topk_ids int32 [T, k]; ids outside [0, E) are not
+ * counted) and p_t = softmax(logits_t):
+ *   loss[0] = balance_coef / num_seqs * sum_s sum_e (E c_{s,e} / (k n_s)) (mean_t p_{t,e})
+ *   loss[1] = z_coef / num_seqs * sum_s mean_t (log sum_e exp(logits_{t,e}))^2
+ * A sequence without valid tokens counts as 0; tokens in no sequence and masked
+ * tokens have no part (a masked token's logits are not read).  Logits may be
+ * -inf (an expert that is switched off), but not a whole row of them.
+ * Outputs: loss fp32 [2], counts int32 [num_seqs, E], tokens int32 [num_seqs]
+ * (n_s).  The results do not depend on scheduling.  1 <= E <= 1024, 1 <= k <=
+ * min(E, 32), T k <= 2^24, num_seqs <= 65536 (else MOE_ERR_UNSUPPORTED); T == 0
+ * is a no-op.  ws: moe_balance_loss_workspace_bytes(T, E, num_seqs) bytes (0
+ * for unsupported arguments), aligned to 256; need not be cleared, and calls
+ * that share it must be stream-ordered. */
+MOE_API size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t E, int32_t num_seqs);
+MOE_API moe_status moe_balance_loss(int32_t T, int32_t E, int32_t k, const float* logits, const int32_t* topk_ids,
+                                    const uint8_t* token_mask, int32_t num_seqs, const int32_t* seq_offsets,
+                                    float balance_coef, float z_coef, float* loss, int32_t* counts, int32_t* tokens,
+                                    void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Gradient of the router's logits, d_logits fp32 [T, E], through
+ *   - the top-k weights of moe_route: d_topk_w fp32 [T, k] with topk_w and
+ *     topk_ids (ids outside [0, E) get nothing, an id that a row holds twice
+ *     gets both parts); NULL: none;
+ *   - the losses of moe_balance_loss: d_loss fp32 [2] on the device, with
+ *     counts and tokens as moe_balance_loss wrote them for the same batch
+ *     (counts are constants of the gradient); NULL: none.
+ * At least one of the two is given.  A masked token's row is zero, and nothing
+ * of the token is read.  d_logits must not overlap the inputs.  Limits as
+ * above; no workspace. */
+MOE_API moe_status moe_route_backward(int32_t T, int32_t E, int32_t k, const float* logits, const int32_t* topk_ids,
+                                      const float* topk_w, const float* d_topk_w, const uint8_t* token_mask,
+                                      int32_t num_seqs, const int32_t* seq_offsets, float balance_coef, float z_coef,
+                                      const int32_t* counts, const int32_t* tokens, const float* d_loss,
+                                      float* d_logits, hipStream_t stream);
+
 /* Size of the device scratch array behind moe_forward_noalloc (64 MiB per
  * device, held until the process ends). */
 #define MOE_NOALLOC_SCRATCH_BYTES (64u << 20)

@@ -55,6 +55,14 @@ EXPORTED = [
     "moe_nvfp4_linear_workspace_bytes",
     "moe_nvfp4_linear_prepare",
     "moe_nvfp4_linear",
+    "moe_fp8_quantize_weights",
+    "moe_fp8_linear_workspace_bytes",
+    "moe_fp8_linear",
+    "moe_fp8_experts_workspace_bytes",
+    "moe_fp8_experts",
+    "moe_balance_loss_workspace_bytes",
+    "moe_balance_loss",
+    "moe_route_backward",
 ]
 
 
@@ -119,6 +127,7 @@ def _load():
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m mixture_experts_layer_sort_amd.build`")
     lib = ctypes.CDLL(LIB_PATH)
     P, S, I32, SZ = ctypes.c_void_p, ctypes.POINTER(moe_shape), ctypes.c_int32, ctypes.c_size_t
+    I64, F32 = ctypes.c_int64, ctypes.c_float
     sig = {
         "moe_status_string": (ctypes.c_char_p, [I32]),
         "moe_check_shape": (I32, [S]),
@@ -152,6 +161,14 @@ def _load():
         "moe_nvfp4_linear_prepare": (I32, [I32, I32, P, P, P, P, SZ, P]),
         "moe_nvfp4_linear": (I32, [I32, I32, I32, P, P, P, P, SZ, P]),
         "moe_workspace_init": (I32, [S, P, SZ, P]),
+        "moe_fp8_quantize_weights": (I32, [I32, I32, I32, P, P, P, P]),
+        "moe_fp8_linear_workspace_bytes": (SZ, [I32, I32, I32]),
+        "moe_fp8_linear": (I32, [I32, I32, I32, P, P, P, I64, P, I64, P, SZ, P]),
+        "moe_fp8_experts_workspace_bytes": (SZ, [S]),
+        "moe_fp8_experts": (I32, [S, I32, P, P, P, P, P, P, P, P, P, SZ, P]),
+        "moe_balance_loss_workspace_bytes": (SZ, [I32, I32, I32]),
+        "moe_balance_loss": (I32, [I32, I32, I32, P, P, P, I32, P, F32, F32, P, P, P, P, SZ, P]),
+        "moe_route_backward": (I32, [I32, I32, I32, P, P, P, P, P, I32, P, F32, F32, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -380,3 +397,56 @@ def moe_nvfp4_linear(M, N, K, packed, x, out, ws, ws_bytes=None, stream=None):
     nbytes = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
     _check(_lib.moe_nvfp4_linear(M, N, K, _ptr(packed), _ptr(x), _ptr(out), _ptr(ws), nbytes, _stream(stream)),
            "moe_nvfp4_linear")
+
+
+def moe_fp8_quantize_weights(count, rows, K, w, codes, scales, stream=None):
+    """e4m3 codes u8 [count, rows, K] and fp32 scales per 128 x 128 block of fp32 matrices w [count, rows, K]."""
+    _check(_lib.moe_fp8_quantize_weights(count, rows, K, _ptr(w), _ptr(codes), _ptr(scales), _stream(stream)),
+           "moe_fp8_quantize_weights")
+
+
+def moe_fp8_linear_workspace_bytes(max_M: int, N: int, K: int) -> int:
+    return _lib.moe_fp8_linear_workspace_bytes(max_M, N, K)
+
+
+def moe_fp8_linear(M, N, K, codes, scales, x, out, ws, x_stride=None, out_stride=None, ws_bytes=None, stream=None):
+    """out bf16 [M, N] = quant(x bf16 [M, K]) . W^T on block-128 fp8 weights; row strides in elements (default K, N)."""
+    nbytes = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check(_lib.moe_fp8_linear(M, N, K, _ptr(codes), _ptr(scales), _ptr(x), K if x_stride is None else x_stride,
+                               _ptr(out), N if out_stride is None else out_stride, _ptr(ws), nbytes,
+                               _stream(stream)), "moe_fp8_linear")
+
+
+def moe_fp8_experts_workspace_bytes(shape: moe_shape) -> int:
+    return _lib.moe_fp8_experts_workspace_bytes(ctypes.byref(shape))
+
+
+def moe_fp8_experts(shape, T, w13_codes, w13_scales, w2_codes, w2_scales, offsets, sorted_pairs, x, y, ws,
+                    ws_bytes=None, stream=None):
+    """Expert MLPs of routed tokens on block-128 fp8 weights: y bf16 [T * top_k, H], rows by pair."""
+    nbytes = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check(_lib.moe_fp8_experts(ctypes.byref(shape), T, _ptr(w13_codes), _ptr(w13_scales), _ptr(w2_codes),
+                                _ptr(w2_scales), _ptr(offsets), _ptr(sorted_pairs), _ptr(x), _ptr(y), _ptr(ws),
+                                nbytes, _stream(stream)), "moe_fp8_experts")
+
+
+def moe_balance_loss_workspace_bytes(T: int, E: int, num_seqs: int = 1) -> int:
+    return _lib.moe_balance_loss_workspace_bytes(T, E, num_seqs)
+
+
+def moe_balance_loss(T, E, k, logits, topk_ids, loss, counts, tokens, ws, balance_coef, z_coef=0.0, token_mask=None,
+                     num_seqs=1, seq_offsets=None, ws_bytes=None, stream=None):
+    """loss fp32 [2] = balance loss and router z-loss; counts int32 [num_seqs, E], tokens int32 [num_seqs]."""
+    nbytes = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check(_lib.moe_balance_loss(T, E, k, _ptr(logits), _ptr(topk_ids), _ptr(token_mask), num_seqs,
+                                 _ptr(seq_offsets), balance_coef, z_coef, _ptr(loss), _ptr(counts), _ptr(tokens),
+                                 _ptr(ws), nbytes, _stream(stream)), "moe_balance_loss")
+
+
+def moe_route_backward(T, E, k, logits, topk_ids, d_logits, topk_w=None, d_topk_w=None, d_loss=None, counts=None,
+                       tokens=None, balance_coef=0.0, z_coef=0.0, token_mask=None, num_seqs=1, seq_offsets=None,
+                       stream=None):
+    """d_logits fp32 [T, E] through the top-k weights (d_topk_w) and the losses of moe_balance_loss (d_loss)."""
+    _check(_lib.moe_route_backward(T, E, k, _ptr(logits), _ptr(topk_ids), _ptr(topk_w), _ptr(d_topk_w),
+                                   _ptr(token_mask), num_seqs, _ptr(seq_offsets), balance_coef, z_coef, _ptr(counts),
+                                   _ptr(tokens), _ptr(d_loss), _ptr(d_logits), _stream(stream)), "moe_route_backward")

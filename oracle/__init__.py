@@ -32,4 +32,7 @@ Modules:
   quant   - MXFP8 / NVFP4 block quantisers (activations and weights)
   moe     - routing, permutation, the layer (per-token loop and
             expert-grouped forms)
+  linear  - dense NVFP4 linear layer
+  fp8_block - products on block-128 fp8 weights, dense and over experts
+  router  - balance loss, router z-loss and the logits' gradient
 """
