@@ -137,6 +137,12 @@ hipError_t launch_fp8_quantize_weights(int count, int rows, int K, const float* 
 // xq [M][Kp], xs [Kp / 128][M] of x's M rows, Kp = K rounded up to 128 (columns past K: zero codes)
 hipError_t launch_fp8_quantize_rows(int M, int K, const uint16_t* x, long long ldx, uint8_t* xq, float* xs,
                                     hipStream_t s);
+// The same, and beside it the token tiles of `tile` sorted rows of every expert: tiles[i] = (expert, first row).
+hipError_t launch_fp8_quantize_tokens(int T, int K, const uint16_t* x, uint8_t* xq, float* xs, const int* offsets,
+                                      int E, int tile, int2* tiles, int* ntiles, hipStream_t s);
+// The tiled kernel (many token rows; reads codes).  token_tiles: grouped modes, at least the number of tiles.
+hipError_t launch_fp8_tile(Fp8Mode mode, const Fp8Args& a, long long token_tiles, hipStream_t s);
+int fp8_tile_tokens();
 // The streaming kernel (few token rows per weight matrix; quantises x itself).
 hipError_t launch_fp8_stream(Fp8Mode mode, const Fp8Args& a, int cus, hipStream_t s);
 

@@ -46,17 +46,26 @@ LinearWorkspace linear_workspace(size_t M, size_t K) {
   return w;
 }
 
-// experts: codes and scales of x, then the intermediate (bf16 rows, or codes and scales)
+// experts: codes and scales of x, the intermediate (bf16 rows of the streaming kernel; codes and scales of the tiled
+// one: I + I / 32 bytes a row, less than the 2 I of bf16), and the token tiles
 struct ExpertsWorkspace {
-  size_t xq, xs, h, total;
+  size_t xq, xs, h, hs, tiles, ntiles, total;
 };
+// token tiles of `pairs` sorted rows, at most: every expert that has rows may end inside one
+size_t max_tiles(const moe_shape* s, size_t pairs) {
+  const size_t E = s->num_experts;
+  return pairs / fp8_tile_tokens() + (pairs < E ? pairs : E);
+}
 ExpertsWorkspace experts_workspace(const moe_shape* s) {
   const size_t T = s->max_tokens, H = s->hidden, P = T * s->top_k, I = s->inter;
   ExpertsWorkspace w;
   w.xq = 0;
   w.xs = up256(T * H);
   w.h = w.xs + up256(T * (H / kFp8Blk) * sizeof(float));
-  w.total = w.h + up256(P * I * 2);
+  w.hs = w.h + up256(P * I);
+  w.tiles = w.h + up256(P * I) + up256(P * I);
+  w.ntiles = w.tiles + up256(max_tiles(s, P) * sizeof(int2));
+  w.total = w.ntiles + 256;
   return w;
 }
 
@@ -117,7 +126,16 @@ moe_status moe_fp8_linear(int32_t M, int32_t N, int32_t K, const void* codes, co
   a.out = out;
   a.ldo = out_stride;
   a.rows = M, a.E = 1, a.N = N, a.K = K, a.k = 1;
-  return launched(launch_fp8_stream(FP8_DENSE, a, cu_count(), stream));
+  if (M <= 64) return launched(launch_fp8_stream(FP8_DENSE, a, cu_count(), stream));
+  const LinearWorkspace W = linear_workspace(M, K);
+  uint8_t* xq = (uint8_t*)ws + W.xq;
+  float* xs = (float*)((uint8_t*)ws + W.xs);
+  hipError_t e = launch_fp8_quantize_rows(M, K, x, x_stride, xq, xs, stream);
+  if (e != hipSuccess) return MOE_ERR_LAUNCH;
+  a.xq = xq;
+  a.xs = xs;
+  a.xrows = M;
+  return launched(launch_fp8_tile(FP8_DENSE, a, 0, stream));
 }
 
 size_t moe_fp8_experts_workspace_bytes(const moe_shape* shape) {
@@ -151,7 +169,36 @@ moe_status moe_fp8_experts(const moe_shape* s, int32_t T, const void* w13_codes,
   a.ldo = s->inter;
   a.rows = T * s->top_k, a.E = s->num_experts, a.N = 2 * s->inter, a.K = s->hidden, a.k = s->top_k;
   a.limit = s->gate_up_limit;
-  hipError_t e = launch_fp8_stream(FP8_GATE_UP, a, cus, stream);
+  hipError_t e;
+  // the tiled kernel from 64 rows per expert on; its gathered rows are addressed with 32 bits
+  const long long P = (long long)T * s->top_k;
+  if (P >= 64LL * s->num_experts && (long long)T * s->hidden < (1LL << 31)) {
+    float* xs = (float*)(base + W.xs);
+    int2* tiles = (int2*)(base + W.tiles);
+    int* ntiles = (int*)(base + W.ntiles);
+    e = launch_fp8_quantize_tokens(T, s->hidden, x, base + W.xq, xs, offsets, s->num_experts, fp8_tile_tokens(), tiles,
+                                   ntiles, stream);
+    if (e != hipSuccess) return MOE_ERR_LAUNCH;
+    a.xq = base + W.xq;
+    a.xs = xs;
+    a.xrows = T;
+    a.tiles = tiles;
+    a.ntiles = ntiles;
+    a.hq = base + W.h;
+    a.hs = (float*)(base + W.hs);
+    e = launch_fp8_tile(FP8_GATE_UP, a, max_tiles(s, P), stream);
+    if (e != hipSuccess) return MOE_ERR_LAUNCH;
+    a.w = (const uint8_t*)w2_codes;
+    a.wsc = w2_scales;
+    a.xq = a.hq;
+    a.xs = a.hs;
+    a.xrows = a.rows;
+    a.out = y;
+    a.ldo = s->hidden;
+    a.N = s->hidden, a.K = s->inter;
+    return launched(launch_fp8_tile(FP8_DOWN, a, max_tiles(s, P), stream));
+  }
+  e = launch_fp8_stream(FP8_GATE_UP, a, cus, stream);
   if (e != hipSuccess) return MOE_ERR_LAUNCH;
   a.w = (const uint8_t*)w2_codes;
   a.wsc = w2_scales;

@@ -36,7 +36,104 @@ __global__ __launch_bounds__(256) void fp8_quantize_weights_kernel(int rows, int
   if (tid == 0) scales[blockIdx.x] = m / kFp8Max;
 }
 
+// Rows of x quantised per 128 columns.  A block takes 64 rows x 512 columns: a
+// wave one row of them at a time (16 lanes per 128-column block, 16 bytes
+// each), 16 rows in turn; the 4 x 64 scales go out through LDS as runs of 64
+// (scales are stored column-block-major, so a tile's tokens read them in one
+// piece).  Bound by memory: 2 bytes in, 1 out per value.  The last block of a
+// grouped launch writes the token tiles instead.
+struct TileList {
+  const int* offsets;
+  int E, tile;
+  int2* tiles;
+  int* ntiles;
+};
+
+constexpr int kQRows = 64, kQCols = 512;
+
+__device__ __forceinline__ void write_tiles(const TileList& l) {
+  __shared__ int part[4];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  int base = 0;
+  for (int e0 = 0; e0 < l.E; e0 += 256) {
+    const int e = e0 + tid;
+    int first = 0, c = 0;
+    if (e < l.E) {
+      first = l.offsets[e];
+      c = (max(0, l.offsets[e + 1] - first) + l.tile - 1) / l.tile;
+    }
+    int s = c;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(s, d, 64);
+      if (lane >= d) s += o;
+    }
+    if (lane == 63) part[wv] = s;
+    __syncthreads();
+    int at = base + s - c;
+    for (int i = 0; i < 4; ++i) {
+      if (i < wv) at += part[i];
+      base += part[i];
+    }
+    for (int i = 0; i < c; ++i) l.tiles[at + i] = make_int2(e, first + i * l.tile);
+    __syncthreads();
+  }
+  if (tid == 0) *l.ntiles = base;
+}
+
+__global__ __launch_bounds__(256) void fp8_quantize_rows_kernel(int M, int K, const uint16_t* x, long long ldx,
+                                                                uint8_t* xq, float* xs, TileList list) {
+  __shared__ float sc[4][kQRows];
+  const int KB = (K + kFp8Blk - 1) / kFp8Blk, Kp = KB * kFp8Blk, CB = (Kp + kQCols - 1) / kQCols;
+  if (list.tiles && blockIdx.x == gridDim.x - 1) {
+    write_tiles(list);
+    return;
+  }
+  const int cb = blockIdx.x % CB, m0 = blockIdx.x / CB * kQRows;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int col = cb * kQCols + 8 * lane;
+  constexpr int kPer = kQRows / 4, U = 8;
+  const u32x4 none = {0, 0, 0, 0};
+  for (int i0 = 0; i0 < kPer; i0 += U) {
+    u32x4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int m = min(m0 + wv * kPer + i0 + u, M - 1);
+      v[u] = col < K ? *reinterpret_cast<const u32x4*>(x + (size_t)m * ldx + col) : none;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int row = wv * kPer + i0 + u;
+      const float m = max_row16(fp8_amax8(v[u], kFp8Tiny));
+      const uint2 c = fp8_codes8(v[u], kFp8Max / m);
+      if ((lane & 15) == 0) sc[lane >> 4][row] = m / kFp8Max;
+      if (m0 + row < M && col < Kp) *reinterpret_cast<uint2*>(xq + (size_t)(m0 + row) * Kp + col) = c;
+    }
+  }
+  __syncthreads();
+  const int b = cb * 4 + wv;
+  if (b < KB && m0 + lane < M) xs[(size_t)b * M + m0 + lane] = sc[wv][lane];
+}
+
+hipError_t launch_rows(int M, int K, const uint16_t* x, long long ldx, uint8_t* xq, float* xs, const TileList& list,
+                       hipStream_t s) {
+  const long long KB = (K + kFp8Blk - 1) / kFp8Blk, CB = (KB * kFp8Blk + kQCols - 1) / kQCols;
+  const long long blocks = (M + kQRows - 1) / kQRows * CB + (list.tiles ? 1 : 0);
+  fp8_quantize_rows_kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(M, K, x, ldx, xq, xs, list);
+  return hipGetLastError();
+}
+
 }  // namespace
+
+hipError_t launch_fp8_quantize_rows(int M, int K, const uint16_t* x, long long ldx, uint8_t* xq, float* xs,
+                                    hipStream_t s) {
+  return launch_rows(M, K, x, ldx, xq, xs, TileList{}, s);
+}
+
+hipError_t launch_fp8_quantize_tokens(int T, int K, const uint16_t* x, uint8_t* xq, float* xs, const int* offsets,
+                                      int E, int tile, int2* tiles, int* ntiles, hipStream_t s) {
+  return launch_rows(T, K, x, K, xq, xs, TileList{offsets, E, tile, tiles, ntiles}, s);
+}
 
 hipError_t launch_fp8_quantize_weights(int count, int rows, int K, const float* w, uint8_t* codes, float* scales,
                                        hipStream_t s) {
