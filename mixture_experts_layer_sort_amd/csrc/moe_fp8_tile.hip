@@ -140,11 +140,14 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
     else return wr * (16 * S::RF) + 16 * f;
   };
   const int nbk = (a.N + kFp8Blk - 1) / kFp8Blk;
-  const float* wsc[2];  // GATE_UP: gate and up block; else both the same
+  // (constant address space: scalar loads, which do not wait behind the vector loads in flight)
+  typedef const __attribute__((address_space(4))) float* cfloat_p;
+  cfloat_p wsc[2];  // GATE_UP: gate and up block; else both the same
   {
     const int first = min(n0 + (MODE == FP8_GATE_UP ? wr * 8 * S::RF : wr * 16 * S::RF), nspan - 1);
-    wsc[0] = a.wsc + ((size_t)e * nbk + first / kFp8Blk) * KB;
-    wsc[1] = MODE == FP8_GATE_UP ? a.wsc + ((size_t)e * nbk + (nspan + first) / kFp8Blk) * KB : wsc[0];
+    wsc[0] = (cfloat_p)(uintptr_t)(a.wsc + ((size_t)e * nbk + first / kFp8Blk) * KB);
+    wsc[1] = MODE == FP8_GATE_UP ? (cfloat_p)(uintptr_t)(a.wsc + ((size_t)e * nbk + (nspan + first) / kFp8Blk) * KB)
+                                 : wsc[0];
   }
 
   f32x4 acc[S::RF][S::TF];
@@ -154,16 +157,24 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
     for (int t = 0; t < S::TF; ++t) acc[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int slot0 = (q ^ (r & 7)) * 16, slot1 = slot0 ^ 64;  // pieces q and q + 4 of a row with row % 8 == r % 8
-  auto compute = [&](int kb, auto nt) {
+  const int aoff = (frag_row(0) + r) * 128, boff = S::kA + (16 * wt + r) * 128, xoffs = S::kA + S::kB + (16 * wt + r) * 4;
+  auto compute = [&](int kb, float s0, float s1, auto nt) {
     constexpr int NT = decltype(nt)::value;
     const uint8_t* st = lds + (kb % S::NS) * S::kStage;
-    const float s0 = wsc[0][kb], s1 = MODE == FP8_GATE_UP ? wsc[1][kb] : s0;
-    i32x8 A[S::RF];
+    const uint8_t *pa0 = st + aoff + slot0, *pa1 = st + aoff + slot1;
+    const uint8_t *pb0 = st + boff + slot0, *pb1 = st + boff + slot1, *px = st + xoffs;
+    auto frag = [](const uint8_t* p0, const uint8_t* p1) {
+      const u32x4 lo = *reinterpret_cast<const u32x4*>(p0), hi = *reinterpret_cast<const u32x4*>(p1);
+      return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+    i32x8 A[S::RF], B[NT];
+    float sx[NT];
+    f32x4 z[NT][S::RF];
+    constexpr int kUp = MODE == FP8_GATE_UP ? kSpan * 128 : 0;  // bytes from a gate row to its up row
 #pragma unroll
     for (int f = 0; f < S::RF; ++f) {
-      const uint8_t* p = st + (frag_row(f) + r) * 128;
-      const u32x4 lo = *reinterpret_cast<const u32x4*>(p + slot0), hi = *reinterpret_cast<const u32x4*>(p + slot1);
-      A[f] = i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+      const int o = MODE == FP8_GATE_UP ? (f / (S::RF / 2)) * kUp + (f % (S::RF / 2)) * 2048 : f * 2048;
+      A[f] = frag(pa0 + o, pa1 + o);
     }
     if (kb * kFp8Blk + kFp8Blk > a.K) {  // the last block of a K that ends inside it
       const bool lo = kb * kFp8Blk + 16 * q < a.K, hi = kb * kFp8Blk + 64 + 16 * q < a.K;
@@ -172,19 +183,29 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
 #pragma unroll
         for (int i = 0; i < 8; ++i) A[f][i] = (i < 4 ? lo : hi) ? A[f][i] : 0;
     }
+    // Pipeline over token fragments: fragment t + 1 is read and fragment t - 1 is added while the matrix
+    // instructions of fragment t run.  The scheduling groups keep that order.
+    B[0] = frag(pb0, pb1);
+    sx[0] = *reinterpret_cast<const float*>(px);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int tok = 16 * (t * S::WT + wt) + r;
-      const uint8_t* p = st + S::kA + tok * 128;
-      const u32x4 lo = *reinterpret_cast<const u32x4*>(p + slot0), hi = *reinterpret_cast<const u32x4*>(p + slot1);
-      const i32x8 B = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-      const float sx = *reinterpret_cast<const float*>(st + S::kA + S::kB + tok * 4);
+    for (int t = 0; t <= NT; ++t) {
+      if (t + 1 < NT) {
+        B[t + 1] = frag(pb0 + (t + 1) * S::WT * 2048, pb1 + (t + 1) * S::WT * 2048);
+        sx[t + 1] = *reinterpret_cast<const float*>(px + (t + 1) * S::WT * 64);
+        __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+      }
 #pragma unroll
       for (int f = 0; f < S::RF; ++f) {
-        const f32x4 z = fp8_mfma(A[f], B);
-        const float sc = sx * (f < S::RF / 2 ? s0 : s1);
+        if (t < NT) {
+          z[t][f] = fp8_mfma(A[f], B[t]);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+        if (t > 0) {
+          const float sc = sx[t - 1] * (f < S::RF / 2 ? s0 : s1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[f][t][i] = fmaf(z[i], sc, acc[f][t][i]);
+          for (int i = 0; i < 4; ++i) acc[f][t - 1][i] = fmaf(z[t - 1][f][i], sc, acc[f][t - 1][i]);
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        }
       }
     }
   };
@@ -196,12 +217,17 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
   // one loop per number of token fragments computed (the wave's live ones, rounded up to 1 / 4 of the tile): a
   // bound known at compile time keeps the accumulators in registers
   auto loop = [&](auto nt) {
+    float s0 = wsc[0][0], s1 = wsc[1][0];
     for (int kb = 0; kb < KB; ++kb) {
       // the loads of this step have landed; those of later steps may be in flight
       if (S::NS > 2 && kb + S::NS - 2 < KB) wait_barrier<(S::NS - 2) * kOps>();
       else wait_barrier<0>();
       if (kb + S::NS - 1 < KB) issue(kb + S::NS - 1);
-      compute(kb, nt);
+      const int next = min(kb + 1, KB - 1);
+      const float n0s = wsc[0][next], n1s = wsc[1][next];
+      compute(kb, s0, s1, nt);
+      s0 = n0s;
+      s1 = n1s;
     }
   };
   using std::integral_constant;
