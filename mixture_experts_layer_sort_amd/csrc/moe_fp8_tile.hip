@@ -9,12 +9,24 @@
 // of its issue time) run while another wave of the same SIMD feeds the matrix
 // unit: two waves per SIMD.
 //
-// Both operands reach LDS by 16-byte direct global->LDS loads (buffer form),
-// NS stages of 128-byte rows; piece p of row r lies at slot p ^ (r & 7), which
-// makes the fragment reads (16 rows, one 16-byte piece each per quarter wave)
-// conflict-free.  One barrier per step: a wave waits for its own loads of the
-// step, the barrier says that everyone's have landed and that the stage before
-// is free, then the next loads are issued and the step is computed.
+// Both operands reach LDS by 16-byte direct global->LDS loads (buffer form), a
+// ring of NS stages of 128-byte rows; piece p of row r lies at slot p ^ (r & 7),
+// which makes the fragment reads (16 rows, one 16-byte piece each per quarter
+// wave) conflict-free.  A step's barrier comes two fragments before its end: by
+// then everything of the stage is in registers, so it says both that the next
+// stage has landed and that this one may be refilled, and matrix instructions
+// run on while the next fragments are read.  Loads are issued one by one
+// between matrix instructions (in one run they held the waves up).
+//
+// The 256 x 256 tile has room for two stages only (130 of 160 KB), and its
+// loads, when they come from memory, take longer than a step.  There a stage is
+// refilled in two parts as soon as they are free: X = the weights and the first
+// half of the tokens, free in the middle of the step (the weights are in
+// registers by then), Y = the second half, free at its end.  Either part is
+// issued one and a half steps before its first use, at the price of a second
+// barrier per step:
+//   start(kb): X(kb) has landed, everyone is done with stage kb - 1; Y(kb + 1) is issued
+//   mid(kb):   Y(kb) has landed, everyone is done with X(kb);        X(kb + 2) is issued
 #include "moe_fp8.h"
 
 namespace moe {
@@ -24,23 +36,28 @@ template <int WR_, int WT_, int RF_, int TF_, int NS_>
 struct TileShape {
   static constexpr int WR = WR_, WT = WT_, RF = RF_, TF = TF_, NS = NS_;
   static constexpr int NW = WR * WT, BN = 16 * RF * WR, BT = 16 * TF * WT;
-  static constexpr int kA = BN * 128, kB = BT * 128, kS = BT * 4, kStage = kA + kB + kS;
+  static constexpr int kA = BN * 128, kB = BT * 128, kS = NW * 2 * 256, kStage = kA + kB + kS;
   static constexpr int LA = BN / 8 / NW, LB = BT / 8 / NW;  // 16-byte loads per wave and stage
   static constexpr int kOutBytes = BT * BN * 2;             // bf16 output tile (shares the stages' memory)
   static constexpr int kLds = NS * kStage > kOutBytes ? NS * kStage : kOutBytes;
-  static_assert(BN / 8 % NW == 0 && BT / 8 % NW == 0 && BT / NW <= 64, "loads are dealt evenly");
+  static constexpr bool kTwo = NS == 2;                          // refilled in two parts
+  // vector-memory operations per wave of the two parts (one part: all of them, and none)
+  static constexpr int kX = kTwo ? LA + LB / 2 + 1 : LA + LB + 2, kY = kTwo ? LB / 2 + 1 : 0;
+  static_assert(BN / 8 % NW == 0 && BT / 16 % NW == 0, "loads are dealt evenly");
+  static_assert(TF == 8 || TF == 4, "a half's scales fit a wave");
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, 0x7FFFFFFF, 0x00020000);
+// Direct global->LDS loads of 16 and 4 bytes per lane, at base + off + soff (soff: the same for all lanes).  `bytes`
+// from base on are inside the buffer: a lane whose address lies behind them reads nothing (rows past the end of a
+// tile; their results are dropped).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
 }
-__device__ __forceinline__ void load_lds16(const void* base, uint32_t off, void* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_of(base), (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0,
-                                           0);
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff, void* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, soff, 0, 0);
 }
-__device__ __forceinline__ void load_lds4(const void* base, uint32_t off, void* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_of(base), (__attribute__((address_space(3))) void*)lds, 4, off, 0, 0,
-                                           0);
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff, void* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, off, soff, 0, 0);
 }
 
 // Wait until at most N of this wave's vector-memory operations are
@@ -90,48 +107,77 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
   const int frags = (min(rend - r0, S::BT) + 15) >> 4;
   const int live = (frags - wt + S::WT - 1) / S::WT;
 
-  // this lane's part of the loads: 8 rows of 8 pieces per instruction, row lane / 8, slot lane % 8
+  // Loads.  This lane's part of an instruction: 8 rows of 8 pieces, row lane / 8, slot lane % 8.  Rows are
+  // consecutive, so one lane offset serves all instructions and the rest is scalar; only the gathered rows of
+  // GATE_UP (xq through the pairs) have offsets of their own.
   const int lrow = lane >> 3, piece = (lane & 7) ^ lrow;
-  const uint8_t* wbase;  // GATE_UP: rows [0, BN / 2) of the tile are gate rows, the rest the matching up rows
-  uint32_t woff[S::LA], xoff[S::LB], soff;
-  if constexpr (MODE == FP8_GATE_UP) wbase = a.w + (size_t)e * a.N * a.K;
-  else wbase = a.w + ((size_t)e * a.N + n0) * a.K;
-#pragma unroll
-  for (int j = 0; j < S::LA; ++j) {
-    const int row = 8 * (wv * S::LA + j) + lrow;
-    if constexpr (MODE == FP8_GATE_UP) {
-      const int n = min(n0 + row % kSpan, nspan - 1) + (row / kSpan) * nspan;
-      woff[j] = (uint32_t)n * (uint32_t)a.K;
-    } else {
-      woff[j] = (uint32_t)min(row, a.N - 1 - n0) * (uint32_t)a.K;
-    }
-  }
-  // GATE_UP gathers rows of xq through the pairs; the others read consecutive rows
-  const uint8_t* xbase = MODE == FP8_GATE_UP ? a.xq : a.xq + (size_t)r0 * Kp;
-  const float* sbase = MODE == FP8_GATE_UP ? a.xs : a.xs + r0;
-#pragma unroll
-  for (int j = 0; j < S::LB; ++j) {
-    const int row = min(r0 + 8 * (wv * S::LB + j) + lrow, rend - 1);
-    const uint32_t src = MODE == FP8_GATE_UP ? (uint32_t)(a.pairs[row] / a.k) : (uint32_t)(row - r0);
-    xoff[j] = src * (uint32_t)Kp + 16 * piece;
-  }
-  {
-    const int row = min(r0 + wv * (S::BT / S::NW) + min(lane, S::BT / S::NW - 1), rend - 1);
-    soff = 4u * (MODE == FP8_GATE_UP ? (uint32_t)(a.pairs[row] / a.k) : (uint32_t)(row - r0));
-  }
-  auto issue = [&](int kb) {
-    uint8_t* st = lds + (kb % S::NS) * S::kStage;
-    // pieces past the end of a weight row (K not a multiple of 128) load the block's first piece; they are
-    // cleared in the fragments
-    const uint32_t wp = kb * kFp8Blk + 16 * piece < a.K ? 16u * piece : 0u;
-#pragma unroll
-    for (int j = 0; j < S::LA; ++j)
-      load_lds16(wbase + (size_t)kb * kFp8Blk, woff[j] + wp, st + (wv * S::LA + j) * 1024);
+  // first token row of load j: half of each wave's loads fill the first half of the tile's tokens
+  auto tok_row = [&](int j) { return j / (S::LB / 2) * (S::BT / 2) + 8 * (wv * (S::LB / 2) + j % (S::LB / 2)); };
+  // A wave loads the scales of its own tokens: lane l that of fragment (h TF / 2 + l / 16), token l % 16, of half h
+  // (TF = 4 needs 32 of them; the other lanes repeat them into slots of their own)
+  auto scale_row = [&](int h) { return 16 * ((h * (S::TF / 2) + (lane >> 4) % (S::TF / 2)) * S::WT + wt) + (lane & 15); };
+  const uint32_t wrow = (uint32_t)lrow * (uint32_t)a.K;
+  uint32_t xoff[MODE == FP8_GATE_UP ? S::LB : 1], soff[MODE == FP8_GATE_UP ? 2 : 1];
+  if constexpr (MODE == FP8_GATE_UP) {
 #pragma unroll
     for (int j = 0; j < S::LB; ++j)
-      load_lds16(xbase + (size_t)kb * kFp8Blk, xoff[j], st + S::kA + (wv * S::LB + j) * 1024);
-    if (lane < S::BT / S::NW)
-      load_lds4(sbase + (size_t)kb * a.xrows, soff, st + S::kA + S::kB + wv * (S::BT / S::NW) * 4);
+      xoff[j] = (uint32_t)(a.pairs[min(r0 + tok_row(j) + lrow, rend - 1)] / a.k) * (uint32_t)Kp + 16 * piece;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      soff[h] = 4u * (uint32_t)(a.pairs[min(r0 + scale_row(h), rend - 1)] / a.k);
+  } else {
+    xoff[0] = (uint32_t)lrow * (uint32_t)Kp + 16 * piece;
+    soff[0] = 4 * scale_row(0);
+  }
+  // this wave's weight rows of the tile: 8 LA from row 8 LA wv on (GATE_UP: all gate rows or all up rows)
+  const int wfirst = 8 * S::LA * wv;
+  static_assert(MODE != FP8_GATE_UP || kSpan % (8 * S::LA) == 0, "a wave loads gate rows or up rows");
+  const int wn = MODE == FP8_GATE_UP ? n0 + wfirst % kSpan + wfirst / kSpan * nspan : n0 + wfirst;
+  const uint8_t* wbase = a.w + ((size_t)e * a.N + min(wn, a.N - 1)) * a.K;
+  const int wbytes = min(a.N - wn, 8 * S::LA) * a.K;  // may be negative: no rows
+  const uint8_t* xbase = MODE == FP8_GATE_UP ? a.xq : a.xq + (size_t)r0 * Kp;
+  const float* sbase = MODE == FP8_GATE_UP ? a.xs : a.xs + r0;
+  const int xrows = min(rend - r0, S::BT);
+  // The loads of one step, one by one (X: LA of weights, LB / 2 of tokens, 1 of scales; Y: LB / 2 and 1).  Steps past
+  // the last one load the last one again (into a stage that is not read any more), so that the counts of the waits
+  // hold to the end.
+  auto stage = [&](int step) { return lds + (S::kTwo ? step & 1 : step % S::NS) * S::kStage; };
+  auto load_tokens = [&](int step, int j) {
+    const int kb = min(step, KB - 1), row = tok_row(j);
+    uint8_t* to = stage(step) + S::kA + row * 128;
+    if constexpr (MODE == FP8_GATE_UP)
+      load_lds16(rsrc_of(xbase + kb * kFp8Blk, 0x7FFFFFFF), xoff[j], 0, to);
+    else
+      load_lds16(rsrc_of(xbase + kb * kFp8Blk, (xrows * Kp - kb * kFp8Blk)), xoff[0], row * Kp, to);
+  };
+  auto load_scales = [&](int step, int h) {
+    const int kb = min(step, KB - 1);
+    uint8_t* to = stage(step) + S::kA + S::kB + (wv * 2 + h) * 256;
+    if constexpr (MODE == FP8_GATE_UP)
+      load_lds4(rsrc_of(sbase + (size_t)kb * a.xrows, 0x7FFFFFFF), soff[h], 0, to);
+    else
+      load_lds4(rsrc_of(sbase + (size_t)kb * a.xrows, (xrows * 4)), soff[0], h * (S::BT / 2) * 4, to);
+  };
+  auto issue_x = [&](int step, int i) {
+    if (i < S::LA) {
+      const int kb = min(step, KB - 1);
+      // pieces past the end of a weight row (K not a multiple of 128) load the block's first piece; they are
+      // cleared in the fragments
+      const uint32_t woff = wrow + (kb * kFp8Blk + 16 * piece < a.K ? 16u * piece : 0u);
+      load_lds16(rsrc_of(wbase + kb * kFp8Blk, max(wbytes - kb * kFp8Blk, 0)), woff, 8 * i * a.K,
+                 stage(step) + (wfirst + 8 * i) * 128);
+    } else if (i < S::LA + S::LB / 2) {
+      load_tokens(step, i - S::LA);
+    } else if (i == S::LA + S::LB / 2) {
+      load_scales(step, 0);
+    } else {  // one part only
+      if (i < S::kX - 1) load_tokens(step, i - S::LA - 1);
+      else load_scales(step, 1);
+    }
+  };
+  auto issue_y = [&](int step, int i) {
+    if (i < S::kY - 1) load_tokens(step, S::LB / 2 + i);
+    else load_scales(step, 1);
   };
 
   // weight fragments of this wave: rows of the tile, and their scale rows
@@ -140,14 +186,13 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
     else return wr * (16 * S::RF) + 16 * f;
   };
   const int nbk = (a.N + kFp8Blk - 1) / kFp8Blk;
-  // (constant address space: scalar loads, which do not wait behind the vector loads in flight)
-  typedef const __attribute__((address_space(4))) float* cfloat_p;
-  cfloat_p wsc[2];  // GATE_UP: gate and up block; else both the same
+  // the scales of 64 K blocks at a time in one register, a lane each: a step takes its own by readlane (a load per
+  // step would wait behind the direct-to-LDS loads, a scalar load behind every LDS read)
+  const float* wsc[2];  // GATE_UP: gate and up block; else both the same
   {
     const int first = min(n0 + (MODE == FP8_GATE_UP ? wr * 8 * S::RF : wr * 16 * S::RF), nspan - 1);
-    wsc[0] = (cfloat_p)(uintptr_t)(a.wsc + ((size_t)e * nbk + first / kFp8Blk) * KB);
-    wsc[1] = MODE == FP8_GATE_UP ? (cfloat_p)(uintptr_t)(a.wsc + ((size_t)e * nbk + (nspan + first) / kFp8Blk) * KB)
-                                 : wsc[0];
+    wsc[0] = a.wsc + ((size_t)e * nbk + first / kFp8Blk) * KB;
+    wsc[1] = MODE == FP8_GATE_UP ? a.wsc + ((size_t)e * nbk + (nspan + first) / kFp8Blk) * KB : wsc[0];
   }
 
   f32x4 acc[S::RF][S::TF];
@@ -157,85 +202,143 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
     for (int t = 0; t < S::TF; ++t) acc[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int slot0 = (q ^ (r & 7)) * 16, slot1 = slot0 ^ 64;  // pieces q and q + 4 of a row with row % 8 == r % 8
-  const int aoff = (frag_row(0) + r) * 128, boff = S::kA + (16 * wt + r) * 128, xoffs = S::kA + S::kB + (16 * wt + r) * 4;
-  auto compute = [&](int kb, float s0, float s1, auto nt) {
+  const int aoff = (frag_row(0) + r) * 128, boff = S::kA + (16 * wt + r) * 128, xoffs = S::kA + S::kB + wv * 512 + r * 4;
+  auto frag = [](const uint8_t* p0, const uint8_t* p1) {
+    const u32x4 lo = *reinterpret_cast<const u32x4*>(p0), hi = *reinterpret_cast<const u32x4*>(p1);
+    return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+  };
+  constexpr int kUp = MODE == FP8_GATE_UP ? kSpan * 128 : 0;  // bytes from a gate row to its up row
+  constexpr int kHalfF = S::RF / 2;
+
+  // One loop per number NT of token fragments computed (the wave's live ones, rounded up to a quarter of the tile's):
+  // a bound known at compile time keeps the accumulators in registers.  Every loop has the same barriers.
+  auto loop = [&](auto nt) {
     constexpr int NT = decltype(nt)::value;
-    const uint8_t* st = lds + (kb % S::NS) * S::kStage;
-    const uint8_t *pa0 = st + aoff + slot0, *pa1 = st + aoff + slot1;
-    const uint8_t *pb0 = st + boff + slot0, *pb1 = st + boff + slot1, *px = st + xoffs;
-    auto frag = [](const uint8_t* p0, const uint8_t* p1) {
-      const u32x4 lo = *reinterpret_cast<const u32x4*>(p0), hi = *reinterpret_cast<const u32x4*>(p1);
-      return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-    };
-    i32x8 A[S::RF], B[NT];
-    float sx[NT];
-    f32x4 z[NT][S::RF];
-    constexpr int kUp = MODE == FP8_GATE_UP ? kSpan * 128 : 0;  // bytes from a gate row to its up row
+    constexpr int kStart = NT - 2;                                 // the slots that the barriers come before
+    constexpr int kMid = !S::kTwo ? 0 : NT > S::TF / 2 ? S::TF / 2 - 2 : kStart;
+    i32x8 A[S::RF], B[2];
+    float sx[2];
+    float v0, v1;
+    constexpr int kLead = S::kTwo ? 2 : S::NS - 1;  // steps that X is issued ahead
 #pragma unroll
-    for (int f = 0; f < S::RF; ++f) {
-      const int o = MODE == FP8_GATE_UP ? (f / (S::RF / 2)) * kUp + (f % (S::RF / 2)) * 2048 : f * 2048;
-      A[f] = frag(pa0 + o, pa1 + o);
+    for (int n = 0; n < kLead; ++n) {
+#pragma unroll
+      for (int i = 0; i < S::kX; ++i) issue_x(n, i);
+#pragma unroll
+      for (int i = 0; i < S::kY; ++i)
+        if (n == 0) issue_y(0, i);
     }
-    if (kb * kFp8Blk + kFp8Blk > a.K) {  // the last block of a K that ends inside it
-      const bool lo = kb * kFp8Blk + 16 * q < a.K, hi = kb * kFp8Blk + 64 + 16 * q < a.K;
-#pragma unroll
-      for (int f = 0; f < S::RF; ++f)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) A[f][i] = (i < 4 ? lo : hi) ? A[f][i] : 0;
-    }
-    // Pipeline over token fragments: fragment t + 1 is read and fragment t - 1 is added while the matrix
-    // instructions of fragment t run.  The scheduling groups keep that order.
-    B[0] = frag(pb0, pb1);
-    sx[0] = *reinterpret_cast<const float*>(px);
-#pragma unroll
-    for (int t = 0; t <= NT; ++t) {
-      if (t + 1 < NT) {
-        B[t + 1] = frag(pb0 + (t + 1) * S::WT * 2048, pb1 + (t + 1) * S::WT * 2048);
-        sx[t + 1] = *reinterpret_cast<const float*>(px + (t + 1) * S::WT * 64);
-        __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
-      }
+    constexpr int kInFlight = (kLead - 1) * S::kX + S::kY;  // operations that may be outstanding at a barrier
+    wait_barrier<kInFlight>();  // start(0)
+    {
+      const uint8_t* st = lds;
 #pragma unroll
       for (int f = 0; f < S::RF; ++f) {
-        if (t < NT) {
-          z[t][f] = fp8_mfma(A[f], B[t]);
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        }
-        if (t > 0) {
-          const float sc = sx[t - 1] * (f < S::RF / 2 ? s0 : s1);
+        const int o = MODE == FP8_GATE_UP ? f / kHalfF * kUp + f % kHalfF * 2048 : f * 2048;
+        A[f] = frag(st + aoff + slot0 + o, st + aoff + slot1 + o);
+      }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[f][t - 1][i] = fmaf(z[t - 1][f][i], sc, acc[f][t - 1][i]);
-          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-        }
+      for (int i = 0; i < 2; ++i) {
+        B[i] = frag(st + boff + slot0 + i * S::WT * 2048, st + boff + slot1 + i * S::WT * 2048);
+        sx[i] = *reinterpret_cast<const float*>(st + xoffs + i * 64);
       }
     }
-  };
-
-  constexpr int kOps = S::LA + S::LB + 1;  // vector-memory operations of one stage, per wave
-#pragma unroll
-  for (int i = 0; i < S::NS - 1; ++i)
-    if (i < KB) issue(i);
-  // one loop per number of token fragments computed (the wave's live ones, rounded up to 1 / 4 of the tile): a
-  // bound known at compile time keeps the accumulators in registers
-  auto loop = [&](auto nt) {
-    float s0 = wsc[0][0], s1 = wsc[1][0];
+#pragma unroll 1
     for (int kb = 0; kb < KB; ++kb) {
-      // the loads of this step have landed; those of later steps may be in flight
-      if (S::NS > 2 && kb + S::NS - 2 < KB) wait_barrier<(S::NS - 2) * kOps>();
-      else wait_barrier<0>();
-      if (kb + S::NS - 1 < KB) issue(kb + S::NS - 1);
-      const int next = min(kb + 1, KB - 1);
-      const float n0s = wsc[0][next], n1s = wsc[1][next];
-      compute(kb, s0, s1, nt);
-      s0 = n0s;
-      s1 = n1s;
+      const uint8_t *st = stage(kb), *sn = stage(kb + 1);
+      // (every branch of the step stands before its additions: the compiler would sink them all behind a later one)
+      if ((kb & 63) == 0) {
+        v0 = wsc[0][min(kb + lane, KB - 1)];
+        v1 = MODE == FP8_GATE_UP ? wsc[1][min(kb + lane, KB - 1)] : v0;
+        asm volatile("" : "+v"(v0), "+v"(v1));  // waited for here, not (behind every load in flight) in each step
+      }
+      const float s0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v0), kb & 63));
+      const float s1 = MODE == FP8_GATE_UP ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v1), kb & 63)) : s0;
+      if (kb * kFp8Blk + kFp8Blk > a.K) {  // the last block of a K that ends inside it
+        const bool lo = kb * kFp8Blk + 16 * q < a.K, hi = kb * kFp8Blk + 64 + 16 * q < a.K;
+#pragma unroll
+        for (int f = 0; f < S::RF; ++f)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) A[f][i] = (i < 4 ? lo : hi) ? A[f][i] : 0;
+      }
+      f32x4 z[NT][S::RF];
+      float scl0 = 0.f, scl1 = 0.f;
+      // slot t: matrix instructions of fragment t, additions of fragment t - 1, reads of fragment t + 2
+#pragma unroll
+      for (int t = 0; t <= NT; ++t) {
+        if (t == kMid) {
+          if (kMid == 0) {
+#pragma unroll
+            for (int i = 0; i < S::kY; ++i) issue_y(kb + 1, i);
+          }
+          if (S::kTwo) wait_barrier<kInFlight>();  // mid(kb)
+          if (kMid == kStart) {
+#pragma unroll
+            for (int i = 0; i < S::kX; ++i) issue_x(kb + kLead, i);
+          }
+        }
+        if (t == kStart) wait_barrier<kInFlight>();  // start(kb + 1)
+        __builtin_amdgcn_sched_barrier(0);
+        i32x8 Bn;
+        float sxn = 0.f;
+        if (t < NT) {
+          const uint8_t *sb = t >= kStart ? sn : st;
+          const int tn = t >= kStart ? t - kStart : t + 2;
+          Bn = frag(sb + boff + slot0 + tn * S::WT * 2048, sb + boff + slot1 + tn * S::WT * 2048);
+          sxn = *reinterpret_cast<const float*>(sb + xoffs + tn / (S::TF / 2) * 256 + tn % (S::TF / 2) * 64);
+          __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+        }
+#pragma unroll
+        for (int f = 0; f < S::RF; ++f) {
+          if (t < NT) {
+            z[t][f] = fp8_mfma(A[f], B[t & 1]);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          }
+          if (t > 0) {
+            const float sc = f < kHalfF ? scl0 : scl1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[f][t - 1][i] = fmaf(z[t - 1][f][i], sc, acc[f][t - 1][i]);
+            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+          }
+          // The loads go between matrix instructions: Y over the slots before the mid barrier, X over those between
+          // it and the start barrier.
+          if (f == (S::RF > 1 ? 1 : 0) && t < kStart) {
+            const int slots = t < kMid ? kMid : kStart - kMid, at = t < kMid ? t : t - kMid;
+            const int ops = t < kMid ? S::kY : S::kX;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = at * ops / slots; i < (at + 1) * ops / slots; ++i) {
+              if (t < kMid) issue_y(kb + 1, i);
+              else issue_x(kb + kLead, i);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if (t == NT - 1) {  // this fragment's weights of the next step
+            const int o = MODE == FP8_GATE_UP ? f / kHalfF * kUp + f % kHalfF * 2048 : f * 2048;
+            A[f] = frag(sn + aoff + slot0 + o, sn + aoff + slot1 + o);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+          }
+        }
+        if (t < NT) {
+          scl0 = sx[t & 1] * s0;
+          scl1 = MODE == FP8_GATE_UP ? sx[t & 1] * s1 : scl0;
+          B[t & 1] = Bn;
+          sx[t & 1] = sxn;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   };
   using std::integral_constant;
-  constexpr int kQuarter = S::TF / 4;
-  if (live > 3 * kQuarter) loop(integral_constant<int, S::TF>{});
-  else if (live > 2 * kQuarter) loop(integral_constant<int, 3 * kQuarter>{});
-  else if (live > kQuarter) loop(integral_constant<int, 2 * kQuarter>{});
-  else loop(integral_constant<int, kQuarter>{});
+  if constexpr (S::TF == 8) {
+    if (live > 6) loop(integral_constant<int, 8>{});
+    else if (live > 4) loop(integral_constant<int, 6>{});
+    else if (live > 2) loop(integral_constant<int, 4>{});
+    else loop(integral_constant<int, 2>{});
+  } else {
+    if (live > 2) loop(integral_constant<int, 4>{});
+    else loop(integral_constant<int, 2>{});
+  }
   wait_barrier<0>();  // the stages are free
 
   // accumulator (f, t) element i of lane r + 16 q: tile row frag_row(f) + 4 q + i, token 16 (t WT + wt) + r
