@@ -104,11 +104,39 @@ __device__ __forceinline__ uint32_t fp8_codes4(float a, float b, float c, float 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
-// Largest magnitude of the 8 bf16 values of v (NaN ignored), not below `m`.
-__device__ __forceinline__ float fp8_amax8(const u32x4& v, float m) {
+// Largest magnitudes of the two halves of packed bf16 values, on their bits (magnitudes order like their bits; a NaN
+// is larger than everything and stays).
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+constexpr uint32_t kFp8TinyBits = 0x0D800D80u;  // 2^-100 in both halves
+__device__ __forceinline__ uint32_t bf16x2_amax(uint32_t v, uint32_t m) {
+  u16x2 a, b;
+  v &= 0x7FFF7FFFu;
+  __builtin_memcpy(&a, &v, 4);
+  __builtin_memcpy(&b, &m, 4);
+  const u16x2 c = __builtin_elementwise_max(a, b);
+  uint32_t o;
+  __builtin_memcpy(&o, &c, 4);
+  return o;
+}
+__device__ __forceinline__ uint32_t fp8_amax8(const u32x4& v, uint32_t m) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(v[i])), fabsf(bf16_hi(v[i]))));
+  for (int i = 0; i < 4; ++i) m = bf16x2_amax(v[i], m);
   return m;
+}
+__device__ __forceinline__ float bf16x2_max(uint32_t m) { return fmaxf(bf16_lo(m), bf16_hi(m)); }  // of packed magnitudes
+
+// Factor fp32(448 / m) and scale fp32(m / 448) of a block whose largest magnitude m is a bf16 value >= 2^-100: an
+// approximate quotient and one correction by its remainder.  The remainder is exact, so the corrected quotient is off
+// by 2^-46 relative before its rounding; m has 8 significant bits, so the true quotients are exact or at least 2^-9
+// of an ulp away from a rounding border, and both results are the correctly rounded ones.  (m is scaled down by 2^16
+// for the reciprocal, which is denormal otherwise near the top of the range.)  Infinite or NaN m: both are NaN.
+__device__ __forceinline__ void fp8_factor(float m, float& f, float& s) {
+  const float d = m * 0x1p-16f, r = __builtin_amdgcn_rcpf(d);
+  constexpr float kNum = kFp8Max * 0x1p-16f, kInv = 1.f / kFp8Max;
+  const float f0 = kNum * r;
+  f = fmaf(fmaf(-f0, d, kNum), r, f0);
+  const float s0 = m * kInv;
+  s = fmaf(fmaf(-s0, kFp8Max, m), kInv, s0);
 }
 
 // Codes of the 8 bf16 values of v under the factor f = fp32(448 / amax).
@@ -141,9 +169,11 @@ hipError_t launch_fp8_quantize_rows(int M, int K, const uint16_t* x, long long l
 hipError_t launch_fp8_quantize_tokens(int T, int K, const uint16_t* x, uint8_t* xq, float* xs, const int* offsets,
                                       int E, int tile, int2* tiles, int* ntiles, hipStream_t s);
 // The tiled kernel (many token rows; reads codes).  token_tiles: grouped modes, at least the number of tiles.
-hipError_t launch_fp8_tile(Fp8Mode mode, const Fp8Args& a, long long token_tiles, hipStream_t s);
+hipError_t launch_fp8_tile(Fp8Mode mode, const Fp8Args& a, long long token_tiles, int cus, hipStream_t s);
 int fp8_tile_tokens();
-// The streaming kernel (few token rows per weight matrix; quantises x itself).
+// The streaming kernel (few token rows per weight matrix).  DENSE: reads codes (xq, xs), or with xq null and
+// fp8_decode_fits() quantises x itself; the grouped modes quantise x themselves.
+bool fp8_decode_fits(int M, int K);
 hipError_t launch_fp8_stream(Fp8Mode mode, const Fp8Args& a, int cus, hipStream_t s);
 
 }  // namespace moe

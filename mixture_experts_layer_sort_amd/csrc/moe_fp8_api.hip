@@ -126,7 +126,7 @@ moe_status moe_fp8_linear(int32_t M, int32_t N, int32_t K, const void* codes, co
   a.out = out;
   a.ldo = out_stride;
   a.rows = M, a.E = 1, a.N = N, a.K = K, a.k = 1;
-  if (M <= 64) return launched(launch_fp8_stream(FP8_DENSE, a, cu_count(), stream));
+  if (fp8_decode_fits(M, K)) return launched(launch_fp8_stream(FP8_DENSE, a, cu_count(), stream));
   const LinearWorkspace W = linear_workspace(M, K);
   uint8_t* xq = (uint8_t*)ws + W.xq;
   float* xs = (float*)((uint8_t*)ws + W.xs);
@@ -135,7 +135,8 @@ moe_status moe_fp8_linear(int32_t M, int32_t N, int32_t K, const void* codes, co
   a.xq = xq;
   a.xs = xs;
   a.xrows = M;
-  return launched(launch_fp8_tile(FP8_DENSE, a, 0, stream));
+  if (M <= 32) return launched(launch_fp8_stream(FP8_DENSE, a, cu_count(), stream));
+  return launched(launch_fp8_tile(FP8_DENSE, a, 0, cu_count(), stream));
 }
 
 size_t moe_fp8_experts_workspace_bytes(const moe_shape* shape) {
@@ -186,7 +187,7 @@ moe_status moe_fp8_experts(const moe_shape* s, int32_t T, const void* w13_codes,
     a.ntiles = ntiles;
     a.hq = base + W.h;
     a.hs = (float*)(base + W.hs);
-    e = launch_fp8_tile(FP8_GATE_UP, a, max_tiles(s, P), stream);
+    e = launch_fp8_tile(FP8_GATE_UP, a, max_tiles(s, P), cus, stream);
     if (e != hipSuccess) return MOE_ERR_LAUNCH;
     a.w = (const uint8_t*)w2_codes;
     a.wsc = w2_scales;
@@ -196,7 +197,7 @@ moe_status moe_fp8_experts(const moe_shape* s, int32_t T, const void* w13_codes,
     a.out = y;
     a.ldo = s->hidden;
     a.N = s->hidden, a.K = s->inter;
-    return launched(launch_fp8_tile(FP8_DOWN, a, max_tiles(s, P), stream));
+    return launched(launch_fp8_tile(FP8_DOWN, a, max_tiles(s, P), cus, stream));
   }
   e = launch_fp8_stream(FP8_GATE_UP, a, cus, stream);
   if (e != hipSuccess) return MOE_ERR_LAUNCH;

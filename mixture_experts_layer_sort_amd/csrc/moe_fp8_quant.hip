@@ -36,9 +36,10 @@ __global__ __launch_bounds__(256) void fp8_quantize_weights_kernel(int rows, int
   if (tid == 0) scales[blockIdx.x] = m / kFp8Max;
 }
 
-// Rows of x quantised per 128 columns.  A block takes 64 rows x 512 columns: a
+// Rows of x quantised per 128 columns.  A block takes ROWS (64, or 8 where few rows
+// would leave most of the GPU idle) rows x 512 columns: a
 // wave one row of them at a time (16 lanes per 128-column block, 16 bytes
-// each), 16 rows in turn; the 4 x 64 scales go out through LDS as runs of 64
+// each), ROWS / 4 rows in turn; the 4 x ROWS scales go out through LDS as runs
 // (scales are stored column-block-major, so a tile's tokens read them in one
 // piece).  Bound by memory: 2 bytes in, 1 out per value.  The last block of a
 // grouped launch writes the token tiles instead.
@@ -49,7 +50,7 @@ struct TileList {
   int* ntiles;
 };
 
-constexpr int kQRows = 64, kQCols = 512;
+constexpr int kQCols = 512;
 
 __device__ __forceinline__ void write_tiles(const TileList& l) {
   __shared__ int part[4];
@@ -81,6 +82,7 @@ __device__ __forceinline__ void write_tiles(const TileList& l) {
   if (tid == 0) *l.ntiles = base;
 }
 
+template <int kQRows>
 __global__ __launch_bounds__(256) void fp8_quantize_rows_kernel(int M, int K, const uint16_t* x, long long ldx,
                                                                 uint8_t* xq, float* xs, TileList list) {
   __shared__ float sc[4][kQRows];
@@ -92,7 +94,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_rows_kernel(int M, int K, co
   const int cb = blockIdx.x % CB, m0 = blockIdx.x / CB * kQRows;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int col = cb * kQCols + 8 * lane;
-  constexpr int kPer = kQRows / 4, U = 8;
+  constexpr int kPer = kQRows / 4, U = kPer < 8 ? kPer : 8;
   const u32x4 none = {0, 0, 0, 0};
   for (int i0 = 0; i0 < kPer; i0 += U) {
     u32x4 v[U];
@@ -104,22 +106,25 @@ __global__ __launch_bounds__(256) void fp8_quantize_rows_kernel(int M, int K, co
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int row = wv * kPer + i0 + u;
-      const float m = max_row16(fp8_amax8(v[u], kFp8Tiny));
-      const uint2 c = fp8_codes8(v[u], kFp8Max / m);
-      if ((lane & 15) == 0) sc[lane >> 4][row] = m / kFp8Max;
+      float f, s;
+      fp8_factor(max_row16(bf16x2_max(fp8_amax8(v[u], kFp8TinyBits))), f, s);
+      const uint2 c = fp8_codes8(v[u], f);
+      if ((lane & 15) == 0) sc[lane >> 4][row] = s;
       if (m0 + row < M && col < Kp) *reinterpret_cast<uint2*>(xq + (size_t)(m0 + row) * Kp + col) = c;
     }
   }
   __syncthreads();
   const int b = cb * 4 + wv;
-  if (b < KB && m0 + lane < M) xs[(size_t)b * M + m0 + lane] = sc[wv][lane];
+  if (b < KB && lane < kQRows && m0 + lane < M) xs[(size_t)b * M + m0 + lane] = sc[wv][lane];
 }
 
 hipError_t launch_rows(int M, int K, const uint16_t* x, long long ldx, uint8_t* xq, float* xs, const TileList& list,
                        hipStream_t s) {
   const long long KB = (K + kFp8Blk - 1) / kFp8Blk, CB = (KB * kFp8Blk + kQCols - 1) / kQCols;
-  const long long blocks = (M + kQRows - 1) / kQRows * CB + (list.tiles ? 1 : 0);
-  fp8_quantize_rows_kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(M, K, x, ldx, xq, xs, list);
+  const int rows = M <= 1024 ? 8 : 64;
+  const long long blocks = (M + rows - 1) / rows * CB + (list.tiles ? 1 : 0);
+  if (rows == 8) fp8_quantize_rows_kernel<8><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(M, K, x, ldx, xq, xs, list);
+  else fp8_quantize_rows_kernel<64><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(M, K, x, ldx, xq, xs, list);
   return hipGetLastError();
 }
 

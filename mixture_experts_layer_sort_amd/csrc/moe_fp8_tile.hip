@@ -32,18 +32,19 @@
 namespace moe {
 namespace {
 
-template <int WR_, int WT_, int RF_, int TF_, int NS_>
+template <int WR_, int WT_, int RF_, int TF_, int NS_, int KG_ = 1>
 struct TileShape {
-  static constexpr int WR = WR_, WT = WT_, RF = RF_, TF = TF_, NS = NS_;
+  static constexpr int WR = WR_, WT = WT_, RF = RF_, TF = TF_, NS = NS_, KG = KG_;
   static constexpr int NW = WR * WT, BN = 16 * RF * WR, BT = 16 * TF * WT;
   static constexpr int kA = BN * 128, kB = BT * 128, kS = NW * 2 * 256, kStage = kA + kB + kS;
   static constexpr int LA = BN / 8 / NW, LB = BT / 8 / NW;  // 16-byte loads per wave and stage
   static constexpr int kOutBytes = BT * BN * 2;             // bf16 output tile (shares the stages' memory)
-  static constexpr int kLds = NS * kStage > kOutBytes ? NS * kStage : kOutBytes;
+  static constexpr int kRing = NS * kStage, kLds = KG * kRing > kOutBytes ? KG * kRing : kOutBytes;
   static constexpr bool kTwo = NS == 2;                          // refilled in two parts
   // vector-memory operations per wave of the two parts (one part: all of them, and none)
   static constexpr int kX = kTwo ? LA + LB / 2 + 1 : LA + LB + 2, kY = kTwo ? LB / 2 + 1 : 0;
   static_assert(BN / 8 % NW == 0 && BT / 16 % NW == 0, "loads are dealt evenly");
+  static_assert((KG - 1) * BN * BT * 4 <= KG * kRing, "the groups' sums fit the stages");
   static_assert(TF == 8 || TF == 4, "a half's scales fit a wave");
 };
 
@@ -71,12 +72,15 @@ __device__ __forceinline__ void wait_barrier() {
 }
 
 template <class S, Fp8Mode MODE>
-__global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int band) {
-  extern __shared__ __align__(256) uint8_t lds[];
-  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+__global__ __launch_bounds__(64 * S::NW * S::KG) void fp8_tile_kernel(Fp8Args a, int band) {
+  extern __shared__ __align__(256) uint8_t shared[];
+  const int tid = threadIdx.x, lane = tid & 63, gw = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kg = gw / S::NW, wv = gw % S::NW;  // K group, wave in it
+  uint8_t* lds = shared + kg * S::kRing;
   const int r = lane & 15, q = lane >> 4;
   const int wr = wv % S::WR, wt = wv / S::WR;
   const int KB = (a.K + kFp8Blk - 1) / kFp8Blk, Kp = KB * kFp8Blk;
+  const int steps = (KB + S::KG - 1) / S::KG;  // step s of group g: K block s KG + g
   const int nspan = MODE == FP8_GATE_UP ? a.N / 2 : a.N;                // output columns
   constexpr int kSpan = MODE == FP8_GATE_UP ? S::BN / 2 : S::BN;        // per tile
   const int NB = (nspan + kSpan - 1) / kSpan;
@@ -143,7 +147,7 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
   // hold to the end.
   auto stage = [&](int step) { return lds + (S::kTwo ? step & 1 : step % S::NS) * S::kStage; };
   auto load_tokens = [&](int step, int j) {
-    const int kb = min(step, KB - 1), row = tok_row(j);
+    const int kb = min(step * S::KG + kg, KB - 1), row = tok_row(j);
     uint8_t* to = stage(step) + S::kA + row * 128;
     if constexpr (MODE == FP8_GATE_UP)
       load_lds16(rsrc_of(xbase + kb * kFp8Blk, 0x7FFFFFFF), xoff[j], 0, to);
@@ -151,7 +155,7 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
       load_lds16(rsrc_of(xbase + kb * kFp8Blk, (xrows * Kp - kb * kFp8Blk)), xoff[0], row * Kp, to);
   };
   auto load_scales = [&](int step, int h) {
-    const int kb = min(step, KB - 1);
+    const int kb = min(step * S::KG + kg, KB - 1);
     uint8_t* to = stage(step) + S::kA + S::kB + (wv * 2 + h) * 256;
     if constexpr (MODE == FP8_GATE_UP)
       load_lds4(rsrc_of(sbase + (size_t)kb * a.xrows, 0x7FFFFFFF), soff[h], 0, to);
@@ -160,7 +164,7 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
   };
   auto issue_x = [&](int step, int i) {
     if (i < S::LA) {
-      const int kb = min(step, KB - 1);
+      const int kb = min(step * S::KG + kg, KB - 1);
       // pieces past the end of a weight row (K not a multiple of 128) load the block's first piece; they are
       // cleared in the fragments
       const uint32_t woff = wrow + (kb * kFp8Blk + 16 * piece < a.K ? 16u * piece : 0u);
@@ -244,18 +248,21 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
       }
     }
 #pragma unroll 1
-    for (int kb = 0; kb < KB; ++kb) {
-      const uint8_t *st = stage(kb), *sn = stage(kb + 1);
+    for (int step = 0; step < steps; ++step) {
+      const uint8_t *st = stage(step), *sn = stage(step + 1);
+      const int kb = step * S::KG + kg;
       // (every branch of the step stands before its additions: the compiler would sink them all behind a later one)
-      if ((kb & 63) == 0) {
-        v0 = wsc[0][min(kb + lane, KB - 1)];
-        v1 = MODE == FP8_GATE_UP ? wsc[1][min(kb + lane, KB - 1)] : v0;
+      if ((step & 63) == 0) {  // lane l: the scales of step + l; zero behind the last block (a group may run out first)
+        const int i = (step + lane) * S::KG + kg;
+        v0 = i < KB ? wsc[0][min(i, KB - 1)] : 0.f;
+        v1 = MODE == FP8_GATE_UP ? (i < KB ? wsc[1][min(i, KB - 1)] : 0.f) : v0;
         asm volatile("" : "+v"(v0), "+v"(v1));  // waited for here, not (behind every load in flight) in each step
       }
-      const float s0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v0), kb & 63));
-      const float s1 = MODE == FP8_GATE_UP ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v1), kb & 63)) : s0;
-      if (kb * kFp8Blk + kFp8Blk > a.K) {  // the last block of a K that ends inside it
-        const bool lo = kb * kFp8Blk + 16 * q < a.K, hi = kb * kFp8Blk + 64 + 16 * q < a.K;
+      const float s0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v0), step & 63));
+      const float s1 = MODE == FP8_GATE_UP ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v1), step & 63)) : s0;
+      if (min(kb, KB - 1) * kFp8Blk + kFp8Blk > a.K) {  // the last block of a K that ends inside it
+        const int k0 = min(kb, KB - 1) * kFp8Blk;
+        const bool lo = k0 + 16 * q < a.K, hi = k0 + 64 + 16 * q < a.K;
 #pragma unroll
         for (int f = 0; f < S::RF; ++f)
 #pragma unroll
@@ -269,12 +276,12 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
         if (t == kMid) {
           if (kMid == 0) {
 #pragma unroll
-            for (int i = 0; i < S::kY; ++i) issue_y(kb + 1, i);
+            for (int i = 0; i < S::kY; ++i) issue_y(step + 1, i);
           }
           if (S::kTwo) wait_barrier<kInFlight>();  // mid(kb)
           if (kMid == kStart) {
 #pragma unroll
-            for (int i = 0; i < S::kX; ++i) issue_x(kb + kLead, i);
+            for (int i = 0; i < S::kX; ++i) issue_x(step + kLead, i);
           }
         }
         if (t == kStart) wait_barrier<kInFlight>();  // start(kb + 1)
@@ -308,8 +315,8 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = at * ops / slots; i < (at + 1) * ops / slots; ++i) {
-              if (t < kMid) issue_y(kb + 1, i);
-              else issue_x(kb + kLead, i);
+              if (t < kMid) issue_y(step + 1, i);
+              else issue_x(step + kLead, i);
             }
             __builtin_amdgcn_sched_barrier(0);
           }
@@ -340,6 +347,27 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
     else loop(integral_constant<int, 2>{});
   }
   wait_barrier<0>();  // the stages are free
+  if constexpr (S::KG > 1) {  // the groups' sums, in group order
+    float* part = reinterpret_cast<float*>(shared);
+    if (kg > 0) {
+#pragma unroll
+      for (int t = 0; t < S::TF; ++t)
+#pragma unroll
+        for (int f = 0; f < S::RF; ++f)
+          *reinterpret_cast<f32x4*>(part + ((((kg - 1) * S::TF + t) * S::RF + f) * S::NW + wv) * 256 + lane * 4) = acc[f][t];
+    }
+    wait_barrier<0>();
+    if (kg == 0) {
+      for (int g = 0; g < S::KG - 1; ++g)
+#pragma unroll
+        for (int t = 0; t < S::TF; ++t)
+#pragma unroll
+          for (int f = 0; f < S::RF; ++f)
+            acc[f][t] += *reinterpret_cast<const f32x4*>(part + (((g * S::TF + t) * S::RF + f) * S::NW + wv) * 256 + lane * 4);
+    }
+    wait_barrier<0>();
+  }
+  lds = shared;
 
   // accumulator (f, t) element i of lane r + 16 q: tile row frag_row(f) + 4 q + i, token 16 (t WT + wt) + r
   if constexpr (MODE == FP8_GATE_UP) {
@@ -370,8 +398,9 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
       float m = amax[tok];
 #pragma unroll
       for (int w = 1; w < S::WR; ++w) m = fmaxf(m, amax[w * S::BT + tok]);
-      const float f = kFp8Max / m;
-      if (wr == 0 && q == 0 && r0 + tok < rend) a.hs[(size_t)(n0 / kFp8Blk) * a.rows + r0 + tok] = m / kFp8Max;
+      float f, s;
+      fp8_factor(m, f, s);
+      if (wr == 0 && q == 0 && r0 + tok < rend) a.hs[(size_t)(n0 / kFp8Blk) * a.rows + r0 + tok] = s;
 #pragma unroll
       for (int fr = 0; fr < S::RF / 2; ++fr) {
         const int col = wr * (8 * S::RF) + 16 * fr + 4 * q;
@@ -380,7 +409,7 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
       }
     }
     wait_barrier<0>();
-    for (int c = tid; c < S::BT * 8; c += 64 * S::NW) {
+    for (int c = tid; c < S::BT * 8; c += 64 * S::NW * S::KG) {
       const int tok = c >> 3, p = c & 7;
       if (r0 + tok < rend)
         *reinterpret_cast<u32x4*>(a.hq + (size_t)(r0 + tok) * nspan + n0 + 16 * p) =
@@ -389,6 +418,7 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
   } else {
     // through LDS, so that whole token rows are stored: row of BN values, 16-byte pieces at c ^ (token % pieces)
     constexpr int kPieces = S::BN / 8;
+    if (kg == 0)
 #pragma unroll
     for (int t = 0; t < S::TF; ++t) {
       const int tok = 16 * (t * S::WT + wt) + r;
@@ -403,7 +433,7 @@ __global__ __launch_bounds__(64 * S::NW) void fp8_tile_kernel(Fp8Args a, int ban
     }
     wait_barrier<0>();
     const bool vec = a.ldo % 8 == 0 && ((uintptr_t)a.out & 15) == 0;
-    for (int c = tid; c < S::BT * kPieces; c += 64 * S::NW) {
+    for (int c = tid; c < S::BT * kPieces; c += 64 * S::NW * S::KG) {
       const int tok = c / kPieces, p = c % kPieces, n = n0 + 8 * p;
       if (r0 + tok >= rend || n >= a.N) continue;
       const u32x4 v = *reinterpret_cast<const u32x4*>(lds + tok * (S::BN * 2) + ((p ^ (tok & (kPieces - 1))) << 4));
@@ -429,19 +459,50 @@ hipError_t launch_tile(const Fp8Args& a, long long token_tiles, int band, hipStr
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&fp8_tile_kernel<S, MODE>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
   if (e != hipSuccess) return e;
-  fp8_tile_kernel<S, MODE><<<dim3((unsigned)grid), dim3(64 * S::NW), S::kLds, s>>>(a, band);
+  fp8_tile_kernel<S, MODE><<<dim3((unsigned)grid), dim3(64 * S::NW * S::KG), S::kLds, s>>>(a, band);
   return hipGetLastError();
 }
 
-using Big = TileShape<4, 2, 4, 8, 2>;  // 256 x 256
+using Big = TileShape<4, 2, 4, 8, 2>;  // 256 weight rows x 256 tokens
+
+// Tile count of a dense product, rounds of it on `cus` compute units (one block each), and the time of a step
+// (one K block) measured with one round or less.
+template <class S>
+long long dense_cost(const Fp8Args& a, int cus, int ns_per_block) {
+  const long long tiles = (long long)((a.rows + S::BT - 1) / S::BT) * ((a.N + S::BN - 1) / S::BN);
+  return (tiles + cus - 1) / cus * ns_per_block;
+}
+
+// Dense products: large tiles have the fewest operand bytes per product, small ones fill the GPU when there are few,
+// and share K over groups of waves.  The shape with the least rounds x step time is taken (the step times are those
+// of one block per compute unit; measured with 48 x 4096 x 7168 and confirmed within a fifth on 100 x 7168 x 7168,
+// 500 and 1000 x 2816 x 4096, 1000 x 7168 x 7168, 2000 x 1000 x 2000).
+hipError_t launch_dense(const Fp8Args& a, int cus, hipStream_t s) {
+  using T0 = TileShape<2, 1, 1, 4, 3, 4>;  // 32 x 64, K over 4 groups of waves
+  using T1 = TileShape<4, 1, 1, 4, 4, 2>;  // 64 x 64, K over 2
+  using T2 = TileShape<4, 1, 2, 4, 3, 2>;  // 128 x 64, K over 2
+  using T3 = TileShape<4, 2, 2, 4, 4>;     // 128 x 128
+  const long long cost[5] = {dense_cost<T0>(a, cus, 168), dense_cost<T1>(a, cus, 246), dense_cost<T2>(a, cus, 366),
+                             dense_cost<T3>(a, cus, 500), dense_cost<Big>(a, cus, 980)};
+  int best = 4;
+  for (int i = 3; i >= 0; --i)
+    if (cost[i] < cost[best]) best = i;
+  switch (best) {
+    case 0: return launch_tile<T0, FP8_DENSE>(a, (a.rows + T0::BT - 1) / T0::BT, 4, s);
+    case 1: return launch_tile<T1, FP8_DENSE>(a, (a.rows + T1::BT - 1) / T1::BT, 4, s);
+    case 2: return launch_tile<T2, FP8_DENSE>(a, (a.rows + T2::BT - 1) / T2::BT, 4, s);
+    case 3: return launch_tile<T3, FP8_DENSE>(a, (a.rows + T3::BT - 1) / T3::BT, 4, s);
+    default: return launch_tile<Big, FP8_DENSE>(a, (a.rows + Big::BT - 1) / Big::BT, 4, s);
+  }
+}
 
 }  // namespace
 
 int fp8_tile_tokens() { return Big::BT; }
 
-hipError_t launch_fp8_tile(Fp8Mode mode, const Fp8Args& a, long long token_tiles, hipStream_t s) {
+hipError_t launch_fp8_tile(Fp8Mode mode, const Fp8Args& a, long long token_tiles, int cus, hipStream_t s) {
   switch (mode) {
-    case FP8_DENSE: return launch_tile<Big, FP8_DENSE>(a, (a.rows + Big::BT - 1) / Big::BT, 4, s);
+    case FP8_DENSE: return launch_dense(a, cus, s);
     case FP8_GATE_UP: return launch_tile<Big, FP8_GATE_UP>(a, token_tiles, 1, s);
     default: return launch_tile<Big, FP8_DOWN>(a, token_tiles, 1, s);
   }
