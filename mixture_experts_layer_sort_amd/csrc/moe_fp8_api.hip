@@ -52,9 +52,9 @@ struct ExpertsWorkspace {
   size_t xq, xs, h, hs, tiles, ntiles, total;
 };
 // token tiles of `pairs` sorted rows, at most: every expert that has rows may end inside one
-size_t max_tiles(const moe_shape* s, size_t pairs) {
+size_t max_tiles(const moe_shape* s, size_t pairs, int tile) {
   const size_t E = s->num_experts;
-  return pairs / fp8_tile_tokens() + (pairs < E ? pairs : E);
+  return pairs / tile + (pairs < E ? pairs : E);
 }
 ExpertsWorkspace experts_workspace(const moe_shape* s) {
   const size_t T = s->max_tokens, H = s->hidden, P = T * s->top_k, I = s->inter;
@@ -64,7 +64,7 @@ ExpertsWorkspace experts_workspace(const moe_shape* s) {
   w.h = w.xs + up256(T * (H / kFp8Blk) * sizeof(float));
   w.hs = w.h + up256(P * I);
   w.tiles = w.h + up256(P * I) + up256(P * I);
-  w.ntiles = w.tiles + up256(max_tiles(s, P) * sizeof(int2));
+  w.ntiles = w.tiles + up256(max_tiles(s, P, kFp8TileTokensMin) * sizeof(int2));
   w.total = w.ntiles + 256;
   return w;
 }
@@ -136,7 +136,7 @@ moe_status moe_fp8_linear(int32_t M, int32_t N, int32_t K, const void* codes, co
   a.xs = xs;
   a.xrows = M;
   if (M <= 32) return launched(launch_fp8_stream(FP8_DENSE, a, cu_count(), stream));
-  return launched(launch_fp8_tile(FP8_DENSE, a, 0, cu_count(), stream));
+  return launched(launch_fp8_tile(FP8_DENSE, a, 0, 0, cu_count(), stream));
 }
 
 size_t moe_fp8_experts_workspace_bytes(const moe_shape* shape) {
@@ -171,13 +171,17 @@ moe_status moe_fp8_experts(const moe_shape* s, int32_t T, const void* w13_codes,
   a.rows = T * s->top_k, a.E = s->num_experts, a.N = 2 * s->inter, a.K = s->hidden, a.k = s->top_k;
   a.limit = s->gate_up_limit;
   hipError_t e;
-  // the tiled kernel from 64 rows per expert on; its gathered rows are addressed with 32 bits
+  // The tiled kernel; where its tiles (128 intermediate columns each) would leave half of the compute units idle, and
+  // for gathered rows beyond its 32-bit addresses, the streaming one (T = 1, top-8, H 7168, I 2048: 84 us against 90;
+  // top-2, H 1024, I 512: 14 against 22).
   const long long P = (long long)T * s->top_k;
-  if (P >= 64LL * s->num_experts && (long long)T * s->hidden < (1LL << 31)) {
+  if (P * (s->inter / 128) > cus / 2 && (long long)T * s->hidden < (1LL << 31)) {
+    const int tile = fp8_tile_tokens(P, s->num_experts);
+    const long long ntok = (long long)max_tiles(s, P, tile);
     float* xs = (float*)(base + W.xs);
     int2* tiles = (int2*)(base + W.tiles);
     int* ntiles = (int*)(base + W.ntiles);
-    e = launch_fp8_quantize_tokens(T, s->hidden, x, base + W.xq, xs, offsets, s->num_experts, fp8_tile_tokens(), tiles,
+    e = launch_fp8_quantize_tokens(T, s->hidden, x, base + W.xq, xs, offsets, s->num_experts, tile, tiles,
                                    ntiles, stream);
     if (e != hipSuccess) return MOE_ERR_LAUNCH;
     a.xq = base + W.xq;
@@ -187,7 +191,7 @@ moe_status moe_fp8_experts(const moe_shape* s, int32_t T, const void* w13_codes,
     a.ntiles = ntiles;
     a.hq = base + W.h;
     a.hs = (float*)(base + W.hs);
-    e = launch_fp8_tile(FP8_GATE_UP, a, max_tiles(s, P), cus, stream);
+    e = launch_fp8_tile(FP8_GATE_UP, a, tile, ntok, cus, stream);
     if (e != hipSuccess) return MOE_ERR_LAUNCH;
     a.w = (const uint8_t*)w2_codes;
     a.wsc = w2_scales;
@@ -197,7 +201,7 @@ moe_status moe_fp8_experts(const moe_shape* s, int32_t T, const void* w13_codes,
     a.out = y;
     a.ldo = s->hidden;
     a.N = s->hidden, a.K = s->inter;
-    return launched(launch_fp8_tile(FP8_DOWN, a, max_tiles(s, P), cus, stream));
+    return launched(launch_fp8_tile(FP8_DOWN, a, tile, ntok, cus, stream));
   }
   e = launch_fp8_stream(FP8_GATE_UP, a, cus, stream);
   if (e != hipSuccess) return MOE_ERR_LAUNCH;

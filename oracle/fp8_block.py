@@ -59,11 +59,20 @@ def dequantize_weights(codes, scales):
     return codecs.e4m3_decode(codes).astype(np.float64) * s
 
 
+def _group_max(v):
+    """Largest magnitude of every 8 consecutive columns, [R, ceil(K / 8)]."""
+    R, K = v.shape
+    full = np.zeros((R, -(-K // 8) * 8))
+    full[:, :K] = np.abs(v)
+    return full.reshape(R, -1, 8).max(axis=2)
+
+
 def linear(x_bits, codes, scales):
-    """float64 [M, N] before the output's rounding, and the Euclidean norm of each sum's products."""
+    """float64 [M, N] before the output's rounding, and for each sum the sum over its groups of 8 consecutive products
+    of a bound of the group's largest product (the product of the two operands' largest magnitudes)."""
     xh = dequantize_rows(*quantize_rows(codecs.bf16_decode(np.asarray(x_bits, np.uint16))))
     wh = dequantize_weights(codes, scales)
-    return xh @ wh.T, np.sqrt((xh * xh) @ (wh * wh).T)
+    return xh @ wh.T, _group_max(xh) @ _group_max(wh).T
 
 
 def experts(x_bits, ids, w13, s13, w2, s2, limit=0.0):
