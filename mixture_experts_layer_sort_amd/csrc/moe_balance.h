@@ -30,10 +30,11 @@ struct BalanceWorkspace {
   size_t prob, count, zn, part, ticket, total;
 };
 
-constexpr int kBalanceChunks = 1024;  // token chunks (blocks) of the forward pass, at most
-inline int balance_chunk(int T) {     // tokens per chunk: 4 per wave at least
+constexpr int kBalanceWaves = 4;      // waves per block of the forward pass
+constexpr int kBalanceChunks = 1024;  // token chunks (blocks), at most
+inline int balance_chunk(int T) {     // tokens per chunk: four per wave at least
   const int c = (T + kBalanceChunks - 1) / kBalanceChunks;
-  return c < 16 ? 16 : c;
+  return c < 4 * kBalanceWaves ? 4 * kBalanceWaves : c;
 }
 inline int balance_chunks(int T) { return (T + balance_chunk(T) - 1) / balance_chunk(T); }
 constexpr int kBalanceSlice = 32;     // experts per block of the reduction

@@ -130,6 +130,29 @@ def test_nothing_valid():
     assert not g.any()
 
 
+@pytest.mark.parametrize("T", [30, 400])
+def test_logits_at_the_ends_of_the_type(T):
+    """Rows of only the lowest value, only the largest, and both: no overflow.  (Without the z-loss, whose square is
+    beyond fp32 there.)  Probabilities are 1 / E, 0 or 1 with the usual roundings."""
+    rng, logits, ids, off, mask = _case(T, 96, 3, 2, True, 12)
+    top, low = np.finfo(np.float32).max, np.finfo(np.float32).min
+    logits[1::7] = low
+    logits[2::7] = top
+    logits[3::7] = low
+    logits[3::7, 50] = top
+    loss, counts, tokens = _loss(logits, ids, off, mask, 0.5, 0.0)
+    rl, rc, rt = router.balance_loss(logits, ids, 0.5, 0.0, mask, off)
+    assert np.array_equal(counts.cpu().numpy(), rc) and np.array_equal(tokens.cpu().numpy(), rt)
+    assert rl[1] == 0 and float(loss[1]) == 0
+    assert abs(float(loss[0]) - rl[0]) <= TOL * abs(rl[0])
+    w = rng.random(ids.shape).astype(np.float32)
+    dw = rng.standard_normal(ids.shape).astype(np.float32)
+    ref, mag = router.backward(logits, ids, w, dw, (1.0, 1.0), 0.5, 0.0, mask, off)
+    g = _grad(logits, ids, off, mask, 0.5, 0.0, w, dw, np.ones(2, np.float32), counts, tokens)
+    bad = np.abs(g - ref) > 4 * TOL * mag + 2.0 ** -123
+    assert not bad.any(), (np.argwhere(bad)[:4], g[bad][:4], ref[bad][:4], mag[bad][:4])
+
+
 def test_switched_off_experts_extreme_logits_and_odd_ids():
     """-inf logits and the type's lowest value have probability zero; ids outside are not counted, an id twice is.
     Row 0's exponents reach -87: the difference is rounded at 2^6 2^-24 = 2^-18, its product with log2 e (up to 2^7)
