@@ -205,14 +205,30 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _stream(stream):
-    if stream is None:
-        import torch
+_raw_stream = None
 
-        return torch.cuda.current_stream().cuda_stream
+
+def _stream(stream):
+    """Handle of a stream; None: the current one of the current device."""
+    if stream is None:
+        global _raw_stream
+        if _raw_stream is None:
+            _raw_stream = _find_raw_stream()
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _find_raw_stream():
+    """torch's look-up of the current stream's handle without the Stream object around it, where this torch has it
+    (0.4 us against 3.0: for one token a third of the call)."""
+    import torch
+
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
 
 
 def _check(status: int, what: str):
