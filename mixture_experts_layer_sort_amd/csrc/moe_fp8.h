@@ -49,10 +49,12 @@ struct Fp8Args {
   int xrows;             // rows of xq
   const int* offsets;    // [E + 1] on the device; unused by DENSE
   const int* pairs;      // sorted pairs; unused by DENSE
-  const int2* tiles;     // tile kernel: (expert, first row inside it) of each token tile
+  const int4* tiles;     // tile kernel: each token tile's expert, first row, and the first and number of its group
   const int* ntiles;     // their number
   uint16_t* out;         // bf16 (DENSE: [rows, ldo]; GATE_UP: h [rows, I]; DOWN: y [rows, N])
   long long ldo;
+  float* part;           // streaming kernel, DENSE without codes: sums of each of `splits` runs of K blocks
+  int splits;
   uint8_t* hq;           // tile kernel, GATE_UP: codes [rows, I] and scales [I / 128][rows]
   float* hs;
   int rows, E, N, K, k;
@@ -172,17 +174,24 @@ hipError_t launch_fp8_quantize_weights(int count, int rows, int K, const float* 
 // xq [M][Kp], xs [Kp / 128][M] of x's M rows, Kp = K rounded up to 128 (columns past K: zero codes)
 hipError_t launch_fp8_quantize_rows(int M, int K, const uint16_t* x, long long ldx, uint8_t* xq, float* xs,
                                     hipStream_t s);
-// The same, and beside it the token tiles of `tile` sorted rows of every expert: tiles[i] = (expert, first row).
+// The same, and beside it the token tiles of `tile` sorted rows of every expert, in groups of up to kFp8TileGroup tiles
+// of one expert: tiles[i] = (expert, first row, first tile of the group, tiles in it).
 hipError_t launch_fp8_quantize_tokens(int T, int K, const uint16_t* x, uint8_t* xq, float* xs, const int* offsets,
-                                      int E, int tile, int2* tiles, int* ntiles, hipStream_t s);
+                                      int E, int tile, int4* tiles, int* ntiles, hipStream_t s);
 // The tiled kernel (reads codes).  Grouped modes: `tile` sorted rows per token tile, token_tiles: at least their number.
 hipError_t launch_fp8_tile(Fp8Mode mode, const Fp8Args& a, int tile, long long token_tiles, int cus,
                            hipStream_t s);
 int fp8_tile_tokens(long long rows, int experts);  // sorted rows per tile of the grouped modes
 constexpr int kFp8TileTokensMin = 64;
+constexpr int kFp8TileGroup = 4;  // tiles of an expert that share a weight slab next to each other (8192 tokens: 4.26 -> 4.22 ms)
 // The streaming kernel (few token rows per weight matrix).  DENSE: reads codes (xq, xs), or with xq null and
 // fp8_decode_fits() quantises x itself; the grouped modes quantise x themselves.
 bool fp8_decode_fits(int M, int K);
+// Small dense products: K over `splits` (> 1) runs of blocks, whose sums part [splits][M][N rounded up to 16] a second
+// launch adds; 1: not this way.
+int fp8_splits(int M, int N, int K);
+size_t fp8_split_bytes(int max_M, int N, int K);  // of part for any M <= max_M
+hipError_t launch_fp8_split(const Fp8Args& a, hipStream_t s);
 hipError_t launch_fp8_stream(Fp8Mode mode, const Fp8Args& a, int cus, hipStream_t s);
 
 }  // namespace moe

@@ -2,6 +2,7 @@
 // training operators: host-side argument checks, then launches on the caller's
 // stream.  Nothing here allocates device memory, synchronises or reads device
 // data.
+#include <algorithm>
 #include <atomic>
 
 #include "../../include/moe.h"
@@ -35,14 +36,14 @@ bool fp8_shape_ok(int32_t N, int32_t K) {
 }
 
 struct LinearWorkspace {
-  size_t xq, xs, total;
+  size_t xq, xs, total;  // or the sums of fp8_splits() at 0
 };
-LinearWorkspace linear_workspace(size_t M, size_t K) {
+LinearWorkspace linear_workspace(size_t M, size_t N, size_t K) {
   const size_t kb = (K + kFp8Blk - 1) / kFp8Blk;
   LinearWorkspace w;
   w.xq = 0;
   w.xs = up256(M * kb * kFp8Blk);
-  w.total = w.xs + up256(M * kb * sizeof(float));
+  w.total = std::max(w.xs + up256(M * kb * sizeof(float)), up256(fp8_split_bytes((int)M, (int)N, (int)K)));
   return w;
 }
 
@@ -64,7 +65,7 @@ ExpertsWorkspace experts_workspace(const moe_shape* s) {
   w.h = w.xs + up256(T * (H / kFp8Blk) * sizeof(float));
   w.hs = w.h + up256(P * I);
   w.tiles = w.h + up256(P * I) + up256(P * I);
-  w.ntiles = w.tiles + up256(max_tiles(s, P, kFp8TileTokensMin) * sizeof(int2));
+  w.ntiles = w.tiles + up256(max_tiles(s, P, kFp8TileTokensMin) * sizeof(int4));
   w.total = w.ntiles + 256;
   return w;
 }
@@ -103,7 +104,7 @@ moe_status moe_fp8_quantize_weights(int32_t count, int32_t rows, int32_t K, cons
 
 size_t moe_fp8_linear_workspace_bytes(int32_t max_M, int32_t N, int32_t K) {
   if (max_M < 1 || max_M > (1 << 24) || !fp8_shape_ok(N, K)) return 0;
-  return linear_workspace(max_M, K).total;
+  return linear_workspace(max_M, N, K).total;
 }
 
 moe_status moe_fp8_linear(int32_t M, int32_t N, int32_t K, const void* codes, const float* scales, const uint16_t* x,
@@ -117,7 +118,7 @@ moe_status moe_fp8_linear(int32_t M, int32_t N, int32_t K, const void* codes, co
     return MOE_ERR_INVALID_ARG;
   if (x_stride < K || x_stride % 8 || out_stride < N) return MOE_ERR_INVALID_ARG;
   if (x_stride > (1LL << 32) || out_stride > (1LL << 32)) return MOE_ERR_UNSUPPORTED;
-  if (ws_bytes < linear_workspace(M, K).total) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < linear_workspace(M, N, K).total) return MOE_ERR_WORKSPACE;
   Fp8Args a = {};
   a.w = (const uint8_t*)codes;
   a.wsc = scales;
@@ -126,8 +127,13 @@ moe_status moe_fp8_linear(int32_t M, int32_t N, int32_t K, const void* codes, co
   a.out = out;
   a.ldo = out_stride;
   a.rows = M, a.E = 1, a.N = N, a.K = K, a.k = 1;
+  a.splits = fp8_splits(M, N, K);
+  if (a.splits > 1) {
+    a.part = (float*)ws;
+    return launched(launch_fp8_split(a, stream));
+  }
   if (fp8_decode_fits(M, K)) return launched(launch_fp8_stream(FP8_DENSE, a, cu_count(), stream));
-  const LinearWorkspace W = linear_workspace(M, K);
+  const LinearWorkspace W = linear_workspace(M, N, K);
   uint8_t* xq = (uint8_t*)ws + W.xq;
   float* xs = (float*)((uint8_t*)ws + W.xs);
   hipError_t e = launch_fp8_quantize_rows(M, K, x, x_stride, xq, xs, stream);
@@ -179,7 +185,7 @@ moe_status moe_fp8_experts(const moe_shape* s, int32_t T, const void* w13_codes,
     const int tile = fp8_tile_tokens(P, s->num_experts);
     const long long ntok = (long long)max_tiles(s, P, tile);
     float* xs = (float*)(base + W.xs);
-    int2* tiles = (int2*)(base + W.tiles);
+    int4* tiles = (int4*)(base + W.tiles);
     int* ntiles = (int*)(base + W.ntiles);
     e = launch_fp8_quantize_tokens(T, s->hidden, x, base + W.xq, xs, offsets, s->num_experts, tile, tiles,
                                    ntiles, stream);

@@ -46,7 +46,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_weights_kernel(int rows, int
 struct TileList {
   const int* offsets;
   int E, tile;
-  int2* tiles;
+  int4* tiles;
   int* ntiles;
 };
 
@@ -76,7 +76,10 @@ __device__ __forceinline__ void write_tiles(const TileList& l) {
       if (i < wv) at += part[i];
       base += part[i];
     }
-    for (int i = 0; i < c; ++i) l.tiles[at + i] = make_int2(e, first + i * l.tile);
+    for (int i = 0; i < c; ++i) {
+      const int g = i / kFp8TileGroup * kFp8TileGroup;
+      l.tiles[at + i] = make_int4(e, first + i * l.tile, at + g, min(kFp8TileGroup, c - g));
+    }
     __syncthreads();
   }
   if (tid == 0) *l.ntiles = base;
@@ -136,7 +139,7 @@ hipError_t launch_fp8_quantize_rows(int M, int K, const uint16_t* x, long long l
 }
 
 hipError_t launch_fp8_quantize_tokens(int T, int K, const uint16_t* x, uint8_t* xq, float* xs, const int* offsets,
-                                      int E, int tile, int2* tiles, int* ntiles, hipStream_t s) {
+                                      int E, int tile, int4* tiles, int* ntiles, hipStream_t s) {
   return launch_rows(T, K, x, K, xq, xs, TileList{offsets, E, tile, tiles, ntiles}, s);
 }
 

@@ -75,6 +75,9 @@ __global__ __launch_bounds__(64 * KS) void fp8_stream_kernel(Fp8Args a) {
     total = base;
   }
 
+  constexpr bool kSplit = MODE == FP8_DENSE && !CODES;  // blockIdx.y: the run of K blocks
+  const int run = kSplit ? (KB + a.splits - 1) / a.splits : KB, k0 = kSplit ? blockIdx.y * run : 0;
+  const int k1 = min(KB, k0 + run);
   const long long items = (long long)total * nitems;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
     // tiles of one weight slab run next to each other on one XCD (blocks go round the 8 XCDs)
@@ -215,31 +218,31 @@ __global__ __launch_bounds__(64 * KS) void fp8_stream_kernel(Fp8Args a) {
         }
       }
     };
-    // this wave's steps wv, wv + KS, ...: D of them in flight
-    const int n = wv < KB ? (KB - wv + KS - 1) / KS : 0;
+    // this wave's steps k0 + wv, k0 + wv + KS, ...: D of them in flight
+    const int n = wv < k1 - k0 ? (k1 - k0 - wv + KS - 1) / KS : 0, at = k0 + wv;
     if (n > 0) {
       Step st[D];
 #pragma unroll
       for (int u = 0; u < D; ++u)
-        if (u == 0 || u < n) load(st[u], wv + u * KS);
+        if (u == 0 || u < n) load(st[u], at + u * KS);
       int i = 0;
       for (; i + 2 * D <= n; i += D) {
 #pragma unroll
         for (int u = 0; u < D; ++u) {
-          compute(st[u], wv + (i + u) * KS);
-          load(st[u], wv + (i + u + D) * KS);
+          compute(st[u], at + (i + u) * KS);
+          load(st[u], at + (i + u + D) * KS);
         }
       }
       // fewer than 2 D steps are left, the first D of them loaded
 #pragma unroll
       for (int u = 0; u < D; ++u)
         if (i + u < n) {
-          compute(st[u], wv + (i + u) * KS);
-          if (i + u + D < n) load(st[u], wv + (i + u + D) * KS);
+          compute(st[u], at + (i + u) * KS);
+          if (i + u + D < n) load(st[u], at + (i + u + D) * KS);
         }
 #pragma unroll
       for (int u = 0; u < D - 1; ++u)
-        if (i + u + D < n) compute(st[u], wv + (i + u + D) * KS);
+        if (i + u + D < n) compute(st[u], at + (i + u + D) * KS);
     }
     // waves' partial sums, in wave order; accumulator (f, t) element i of lane r + 16 q is weight row
     // 16 f + 4 q + i, token 16 t + r
@@ -265,6 +268,11 @@ __global__ __launch_bounds__(64 * KS) void fp8_stream_kernel(Fp8Args a) {
         for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], up[i], a.limit);
       }
       if (row < rend) {
+        if constexpr (kSplit) {
+          const int ldp = (a.N + 15) / 16 * 16;
+          *reinterpret_cast<f32x4*>(a.part + ((size_t)blockIdx.y * a.rows + row) * ldp + slab * kItemN + 16 * f + 4 * q) = v;
+          continue;
+        }
         const size_t orow = MODE == FP8_DOWN ? a.pairs[row] : row;
         store4(a.out + orow * (size_t)a.ldo, slab * kItemN + 16 * f + 4 * q, nspan, v);
       }
@@ -377,6 +385,17 @@ __global__ __launch_bounds__(64 * KS) void fp8_decode_kernel(Fp8Args a) {
   }
 }
 
+// out = the runs' sums, added in order: a thread per four columns.
+__global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Args a) {
+  const int quads = (a.N + 15) / 16 * 4, c = blockIdx.x * 256 + threadIdx.x, row = c / quads, n = 4 * (c - row * quads);
+  if (row >= a.rows) return;
+  const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + c;
+  f32x4 v = p[0];
+#pragma unroll 8
+  for (int i = 1; i < a.splits; ++i) v += p[(size_t)i * a.rows * quads];
+  store4(a.out + (size_t)row * a.ldo, n, a.N, v);
+}
+
 template <int NT, int R, int KS, int D, Fp8Mode MODE, bool CODES>
 hipError_t launch_one(const Fp8Args& a, int cus, hipStream_t s) {
   const int span = MODE == FP8_GATE_UP ? a.N / 2 : a.N, per = MODE == FP8_GATE_UP ? 8 * R : 16 * R;
@@ -385,7 +404,8 @@ hipError_t launch_one(const Fp8Args& a, int cus, hipStream_t s) {
   long long grid = tiles * slabs;
   // dense: a block per item; grouped (the number of items is known on the device only): as many as run at once
   if (MODE != FP8_DENSE && grid > 3LL * cus) grid = 3LL * cus;
-  fp8_stream_kernel<NT, R, KS, D, MODE, CODES><<<dim3((unsigned)grid), dim3(64 * KS), 0, s>>>(a);
+  const int runs = MODE == FP8_DENSE && !CODES ? a.splits : 1;
+  fp8_stream_kernel<NT, R, KS, D, MODE, CODES><<<dim3((unsigned)grid, runs), dim3(64 * KS), 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -414,6 +434,41 @@ hipError_t launch_grouped(const Fp8Args& a, int cus, hipStream_t s) {
 // Quantising in every block of the product pays while it is little work (and the launch before it is not): 4 rows of
 // 4096 x 7168 take 11.2 us this way and 11.4 us in two launches, 8 rows 14.5 and 12.3; 8 rows of 7168 x 2048 8.0 and 8.5.
 bool fp8_decode_fits(int M, int K) { return M <= 16 && M * ((K + kFp8Blk - 1) / kFp8Blk) <= 224; }
+
+// Few weight rows and a long K (a low-rank projection): one block per 16 weight rows leaves most of the GPU idle and
+// every wave several trips to memory.  Then K is split over blocks too, runs of at least 8 blocks of 128 (one per wave),
+// as many as fill the compute units; the tokens are quantised where they are used, and a second launch joins the runs
+// (17 rows of 576 x 7168: 8.6 us against 13.3 for quantiser and one block per slab; 64 rows 12.9 against 16.1 for the
+// tiled kernel; 24 of 1024 x 4096 8.1 against 10.3).  One row is faster in one launch (1 x 1024 x 4096: 5.7 us against 6.5).
+constexpr int kSplitRows = 128, kSplitRun = 8, kSplitBlocks = 256;
+
+int fp8_splits(int M, int N, int K) {
+  const int KB = (K + kFp8Blk - 1) / kFp8Blk, most = (KB + kSplitRun - 1) / kSplitRun;
+  if (M > kSplitRows || M * KB <= 64) return 1;
+  const int blocks = (N + 15) / 16 * ((M + 31) / 32);
+  const int n = min(most, kSplitBlocks / blocks);
+  if (n < 2) return 1;
+  const int run = (KB + n - 1) / n;
+  return (KB + run - 1) / run;  // no empty run
+}
+
+size_t fp8_split_bytes(int max_M, int N, int K) {
+  size_t n = 0;
+  for (int M = 32; M < max_M + 32 && M <= kSplitRows; M += 32) {  // fewer rows of as many token tiles need less
+    const int rows = min(M, max_M), splits = fp8_splits(rows, N, K);
+    if (splits > 1) n = max(n, (size_t)splits * rows * ((N + 15) / 16 * 16) * sizeof(float));
+  }
+  return n;
+}
+
+hipError_t launch_fp8_split(const Fp8Args& a, hipStream_t s) {
+  const hipError_t e = a.rows <= 16 ? launch_one<1, 1, 8, 2, FP8_DENSE, false>(a, 0, s)
+                                    : launch_one<2, 1, 8, 2, FP8_DENSE, false>(a, 0, s);
+  if (e != hipSuccess) return e;
+  const long long quads = (long long)a.rows * ((a.N + 15) / 16 * 4);
+  fp8_join_kernel<<<dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
 
 hipError_t launch_fp8_stream(Fp8Mode mode, const Fp8Args& a, int cus, hipStream_t s) {
   switch (mode) {

@@ -101,15 +101,17 @@ __global__ __launch_bounds__(64 * S::NW * S::KG) void fp8_tile_kernel(Fp8Args a,
   const int at = (blockIdx.x & 7) * share + i;
   if (at >= total) return;
   uint8_t* lds = shared + kg * S::kRing;
-  const int bi = at / (band * NB), inb = min(band, MT - bi * band), o = at - bi * band * NB;
-  const int nb = o / inb, mt = bi * band + o % inb;
-
-  int e = 0, r0, rend;
+  int e = 0, r0, rend, nb;
   if constexpr (MODE == FP8_DENSE) {
-    r0 = mt * S::BT;
+    const int bi = at / (band * NB), inb = min(band, MT - bi * band), o = at - bi * band * NB;
+    nb = o / inb;
+    r0 = (bi * band + o % inb) * S::BT;
     rend = a.rows;
   } else {
-    const int2 t = a.tiles[mt];
+    const int4 g = a.tiles[at / NB];  // any tile of the group
+    const int o = at - g.z * NB;
+    nb = o / g.w;
+    const int4 t = a.tiles[g.z + o % g.w];
     e = t.x;
     r0 = t.y;
     rend = a.offsets[e + 1];

@@ -91,6 +91,38 @@ def test_linear(M, N, K):
     assert bool((out[M] == 7.0).all())  # the row behind the last one is left alone
 
 
+# K split over blocks as well (few weight rows, a long K; the last run shorter), with its neighbours that are not split:
+# one row, more weight rows, a K of fewer than 16 blocks, more token rows
+RUNS = [(2, 16, 8208), (5, 7, 5136), (16, 100, 16400), (17, 577, 7168), (40, 33, 2064), (64, 1000, 1040), (128, 250, 4112),
+        (128, 16, 32768), (1, 40, 8208), (20, 4100, 1040), (12, 4100, 4112), (64, 100, 912), (129, 250, 4112)]
+
+
+@pytest.mark.parametrize("M,N,K", RUNS)
+def test_linear_runs_of_k(M, N, K):
+    rng = np.random.default_rng(M * 131 + N + K)
+    x, (c, s) = _x(rng, M, K), _weights(rng, N, K)
+    got, out = _linear(x, c, s, K + 8, N + 3)
+    _check(got, *fb.linear(x, c, s))
+    assert bool((out[:, N:] == 7.0).all()) and bool((out[M] == 7.0).all())
+
+
+def test_linear_one_workspace_for_fewer_rows():
+    """The bytes for max_M rows serve every smaller number, of whichever kernels."""
+    rng, N, K, d = np.random.default_rng(8), 144, 4112, gh.dev()
+    x, (c, s) = _x(rng, 140, K), _weights(rng, N, K)
+    cd, sd, xd = torch.from_numpy(c).to(d), torch.from_numpy(s).to(d), gh.to_device_x(x)
+    ref, groups = fb.linear(x, c, s)
+    size = [lib.moe_fp8_linear_workspace_bytes(m, N, K) for m in range(1, 141)]
+    assert size == sorted(size)
+    ws = torch.full((size[-1],), 0xFF, dtype=torch.uint8, device=d)
+    for M in (140, 1, 128, 3, 16, 33):
+        out = torch.full((M + 1, N), 7.0, dtype=torch.bfloat16, device=d)
+        lib.moe_fp8_linear(M, N, K, cd, sd, xd, out, ws)
+        torch.cuda.synchronize()
+        _check(out[:M].double().cpu().numpy(), ref[:M], groups[:M])
+        assert bool((out[M] == 7.0).all())
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 130, 144), (20, 96, 256), (300, 130, 400), (512, 512, 512)])
 @pytest.mark.parametrize("odd", [1, 8])
 def test_linear_strides(M, N, K, odd):
