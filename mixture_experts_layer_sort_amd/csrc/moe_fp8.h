@@ -58,6 +58,7 @@ struct Fp8Args {
   uint8_t* hq;           // tile kernel, GATE_UP: codes [rows, I] and scales [I / 128][rows]
   float* hs;
   int rows, E, N, K, k;
+  int cap;               // streaming kernel, grouped: rows per tile (<= 16) where the block quantises them, 0: the waves do
   float limit;           // SwiGLU clamp, 0: none
 };
 
@@ -191,6 +192,7 @@ bool fp8_decode_fits(int M, int K);
 // launch adds; 1: not this way.
 int fp8_splits(int M, int N, int K);
 size_t fp8_split_bytes(int max_M, int N, int K);  // of part for any M <= max_M
+int fp8_block_rows(int T, int K);  // Fp8Args::cap of grouped products of T tokens, 0: they do not fit
 hipError_t launch_fp8_split(const Fp8Args& a, hipStream_t s);
 hipError_t launch_fp8_stream(Fp8Mode mode, const Fp8Args& a, int cus, hipStream_t s);
 

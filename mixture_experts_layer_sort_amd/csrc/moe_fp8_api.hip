@@ -177,11 +177,12 @@ moe_status moe_fp8_experts(const moe_shape* s, int32_t T, const void* w13_codes,
   a.rows = T * s->top_k, a.E = s->num_experts, a.N = 2 * s->inter, a.K = s->hidden, a.k = s->top_k;
   a.limit = s->gate_up_limit;
   hipError_t e;
-  // The tiled kernel; where its tiles (128 intermediate columns each) would leave half of the compute units idle, and
-  // for gathered rows beyond its 32-bit addresses, the streaming one (T = 1, top-8, H 7168, I 2048: 84 us against 90;
-  // top-2, H 1024, I 512: 14 against 22).
+  // The tiled kernel; the streaming one for up to 8 tokens (H 7168, I 2048, 256 experts, top-8, T = 4: 248 us against
+  // 258; H 4096, I 1408, 64 experts, top-6, T = 8: 132 against 146; at T = 16 and uneven experts 102 against 77), where
+  // the tiles (128 intermediate columns each) would leave half of the compute units idle, and for gathered rows beyond
+  // the tiled kernel's 32-bit addresses.
   const long long P = (long long)T * s->top_k;
-  if (P * (s->inter / 128) > cus / 2 && (long long)T * s->hidden < (1LL << 31)) {
+  if (T > 8 && P * (s->inter / 128) > cus / 2 && (long long)T * s->hidden < (1LL << 31)) {
     const int tile = fp8_tile_tokens(P, s->num_experts);
     const long long ntok = (long long)max_tiles(s, P, tile);
     float* xs = (float*)(base + W.xs);
@@ -209,6 +210,7 @@ moe_status moe_fp8_experts(const moe_shape* s, int32_t T, const void* w13_codes,
     a.N = s->hidden, a.K = s->inter;
     return launched(launch_fp8_tile(FP8_DOWN, a, tile, ntok, cus, stream));
   }
+  a.cap = fp8_block_rows(T, a.K);
   e = launch_fp8_stream(FP8_GATE_UP, a, cus, stream);
   if (e != hipSuccess) return MOE_ERR_LAUNCH;
   a.w = (const uint8_t*)w2_codes;
@@ -218,6 +220,7 @@ moe_status moe_fp8_experts(const moe_shape* s, int32_t T, const void* w13_codes,
   a.out = y;
   a.ldo = s->hidden;
   a.N = s->hidden, a.K = s->inter;
+  a.cap = fp8_block_rows(T, a.K);
   return launched(launch_fp8_stream(FP8_DOWN, a, cus, stream));
 }
 

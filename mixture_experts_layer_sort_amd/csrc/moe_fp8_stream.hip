@@ -1,15 +1,16 @@
 // Streaming product on block-128 fp8 weights: few token rows per weight
 // matrix (decoding), so the time is that of reading the weights once.
 //
-// Item = (token tile of 16 NT rows, R fragments of 16 weight rows).  The
-// block's KS waves take the 128-wide K blocks in turn; a wave reads its weight
-// fragment straight from the row-major codes into the operand registers (lane
-// r + 16 q: row r, bytes [16 q, 16 q + 16) and [64 + 16 q, + 16) of the block:
-// two loads that together use whole 128-byte lines; which 32 of the 128 bytes
-// a lane holds does not matter, since tokens use the same order) and quantises
-// the tokens' bf16 values of the same block itself: the four lanes of a token
-// share its 128 values, so the block maximum is two exchanges away.  Partial
-// sums of the waves meet in LDS in wave order (the same bits every run).
+// Item = (token tile, R fragments of 16 weight rows).  The block's KS waves
+// take the 128-wide K blocks in turn; a wave reads its weight fragment straight
+// from the row-major codes into the operand registers (lane r + 16 q: row r,
+// bytes [16 q, 16 q + 16) and [64 + 16 q, + 16) of the block; which 32 of the
+// 128 bytes a lane holds does not matter, since tokens use the same order).
+// The two loads of a line are ordinary ones: as non-temporal ones they fetched
+// the line's halves one by one (T = 1 experts, H 7168, I 2048: 76.5 us against
+// 72.2; M = 1, 18432 x 7168: 28.6 against 25.2, 5.2 TB/s).  Partial sums of the
+// waves meet in LDS in wave order (the same bits every run).  More bytes in
+// flight than here (more waves, or more steps per wave) made it slower.
 #include "moe_fp8.h"
 
 namespace moe {
@@ -29,9 +30,36 @@ __device__ __forceinline__ void store4(uint16_t* row, int n, int N, const f32x4&
   }
 }
 
-template <int NT, int R, int KS, int D, Fp8Mode MODE, bool CODES>
+// Where a token's codes come from.  SELF: every wave quantises what it multiplies (the four lanes of a token share a
+// block's 128 values, so the maximum is two exchanges away).  CODES: from memory.  BLOCK: the block quantises its item's
+// rows into LDS while the first weights are on their way (NT = 1, `cap` <= 16 rows per tile; dynamic LDS of
+// block_lds()): the waves' steps are then little more than loads and products (T = 1 experts: 84 -> 77 us).
+enum Fp8Source { SELF, CODES, BLOCK };
+
+__host__ __device__ inline size_t block_lds(int rows, int KB) { return (size_t)KB * 64 + (size_t)rows * (KB * kFp8Blk + 16); }
+
+// Rows `row(i)`, i < rows, of K bf16 values: codes [rows][KB 128 + 16] (row stride K + 16 bytes: the 16 rows of a fragment
+// read start 4 banks apart) and scales [KB][16].  Pieces of 8 values: 16 consecutive lanes have one block of one row.
+template <class F>
+__device__ __forceinline__ void quantize_block(uint8_t* codes, float* scales, int rows, int KB, int K, int tid, int threads,
+                                               F&& row) {
+  const int stride = KB * kFp8Blk + 16;
+  for (int c = tid; c < rows * KB * 16; c += threads) {
+    const int blk = c >> 4, i = blk / KB, kb = blk - i * KB, col = kb * kFp8Blk + 8 * (c & 15);
+    u32x4 v = {0, 0, 0, 0};
+    if (col < K) v = *reinterpret_cast<const u32x4*>(row(i) + col);
+    float f, s;
+    fp8_factor(max_row16(bf16x2_max(fp8_amax8(v, kFp8TinyBits))), f, s);
+    *reinterpret_cast<uint2*>(codes + i * stride + col) = fp8_codes8(v, f);
+    if ((c & 15) == 0) scales[kb * 16 + i] = s;
+  }
+}
+
+template <int NT, int R, int KS, int D, Fp8Mode MODE, Fp8Source SRC>
 __global__ __launch_bounds__(64 * KS) void fp8_stream_kernel(Fp8Args a) {
-  constexpr int kRows = 16 * NT;
+  static_assert(SRC != BLOCK || NT == 1, "one token fragment");
+  extern __shared__ __align__(16) uint8_t quantized[];  // BLOCK
+  const int kRows = SRC == BLOCK ? a.cap : 16 * NT;
   __shared__ f32x4 red[KS][R * NT][64];
   __shared__ int cum[1025];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -75,7 +103,7 @@ __global__ __launch_bounds__(64 * KS) void fp8_stream_kernel(Fp8Args a) {
     total = base;
   }
 
-  constexpr bool kSplit = MODE == FP8_DENSE && !CODES;  // blockIdx.y: the run of K blocks
+  constexpr bool kSplit = MODE == FP8_DENSE && SRC == SELF;  // blockIdx.y: the run of K blocks
   const int run = kSplit ? (KB + a.splits - 1) / a.splits : KB, k0 = kSplit ? blockIdx.y * run : 0;
   const int k1 = min(KB, k0 + run);
   const long long items = (long long)total * nitems;
@@ -103,7 +131,7 @@ __global__ __launch_bounds__(64 * KS) void fp8_stream_kernel(Fp8Args a) {
       }
       e = lo;
       r0 = max(0, a.offsets[e]) + (tile - cum[e]) * kRows;
-      rend = min(a.offsets[e + 1], a.rows);
+      rend = min(min(a.offsets[e + 1], a.rows), r0 + kRows);
     }
     // weight fragments of this lane; rows past the end repeat the last one (results dropped)
     const uint8_t* wrow[R];
@@ -119,14 +147,20 @@ __global__ __launch_bounds__(64 * KS) void fp8_stream_kernel(Fp8Args a) {
     }
     // token rows of this lane
     const uint16_t* xrow[NT];
-    const uint8_t* qrow[NT];  // CODES
+    const uint8_t* qrow[NT];  // CODES, BLOCK
     const float* srow[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+      if constexpr (SRC == BLOCK) {
+        const int i = min(r, rend - r0 - 1);
+        qrow[t] = quantized + KB * 64 + i * (KB * kFp8Blk + 16) + 16 * q;
+        srow[t] = reinterpret_cast<const float*>(quantized) + i;
+        break;
+      }
       const int row = r0 + 16 * t + r;
       int src = min(row, rend - 1);
       if constexpr (MODE == FP8_GATE_UP) src = a.pairs[src] / a.k;
-      if constexpr (CODES) {
+      if constexpr (SRC == CODES) {
         qrow[t] = a.xq + (size_t)src * ((size_t)KB * kFp8Blk) + 16 * q;
         srow[t] = a.xs + src;
       } else {
@@ -141,7 +175,7 @@ __global__ __launch_bounds__(64 * KS) void fp8_stream_kernel(Fp8Args a) {
 
     struct Step {
       u32x4 w[R][2];
-      u32x4 x[NT][CODES ? 2 : 4];
+      u32x4 x[NT][SRC == SELF ? 4 : SRC == CODES ? 2 : 1];
       float s[R], sx[NT];
     };
     // Loads without branches around them (each would end in a wait for everything in flight): rows past the end
@@ -153,18 +187,18 @@ __global__ __launch_bounds__(64 * KS) void fp8_stream_kernel(Fp8Args a) {
 #pragma unroll
       for (int f = 0; f < R; ++f) {
         const uint8_t* p = wrow[f] + (size_t)kb * kFp8Blk;
-        st.w[f][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + lo));
-        st.w[f][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + hi));
+        st.w[f][0] = *reinterpret_cast<const u32x4*>(p + lo);
+        st.w[f][1] = *reinterpret_cast<const u32x4*>(p + hi);
         st.s[f] = wsc[f][kb];
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        if constexpr (CODES) {
+        if constexpr (SRC == CODES) {
           const u32x4* p = reinterpret_cast<const u32x4*>(qrow[t] + (size_t)kb * kFp8Blk);
           st.x[t][0] = p[0];
           st.x[t][1] = p[4];
           st.sx[t] = srow[t][(size_t)kb * a.xrows];
-        } else {
+        } else if constexpr (SRC == SELF) {
           const u32x4* p = reinterpret_cast<const u32x4*>(xrow[t] + (size_t)kb * kFp8Blk + lo);
           const u32x4* p2 = reinterpret_cast<const u32x4*>(xrow[t] + (size_t)kb * kFp8Blk + hi);
           st.x[t][0] = p[0];
@@ -182,15 +216,20 @@ __global__ __launch_bounds__(64 * KS) void fp8_stream_kernel(Fp8Args a) {
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if constexpr (!CODES) st.x[t][j][i] = (j < 2 ? lo : hi) ? st.x[t][j][i] : 0u;
+            if constexpr (SRC == SELF) st.x[t][j][i] = (j < 2 ? lo : hi) ? st.x[t][j][i] : 0u;
     };
     auto compute = [&](Step& st, int kb) {
-      if (!CODES && kb * kFp8Blk + kFp8Blk > a.K) clear_ragged(st, kb);
+      if (SRC == SELF && kb * kFp8Blk + kFp8Blk > a.K) clear_ragged(st, kb);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         i32x8 b;
         float sx;
-        if constexpr (CODES) {
+        if constexpr (SRC == BLOCK) {
+          const u32x4 lo = *reinterpret_cast<const u32x4*>(qrow[t] + kb * kFp8Blk);
+          const u32x4 hi = *reinterpret_cast<const u32x4*>(qrow[t] + kb * kFp8Blk + 64);
+          b = i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+          sx = srow[t][kb * 16];
+        } else if constexpr (SRC == CODES) {
           const u32x4 lo = st.x[t][0], hi = st.x[t][1];
           b = i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
           sx = st.sx[t];
@@ -220,11 +259,21 @@ __global__ __launch_bounds__(64 * KS) void fp8_stream_kernel(Fp8Args a) {
     };
     // this wave's steps k0 + wv, k0 + wv + KS, ...: D of them in flight
     const int n = wv < k1 - k0 ? (k1 - k0 - wv + KS - 1) / KS : 0, at = k0 + wv;
+    Step st[D];
     if (n > 0) {
-      Step st[D];
 #pragma unroll
       for (int u = 0; u < D; ++u)
         if (u == 0 || u < n) load(st[u], at + u * KS);
+    }
+    if constexpr (SRC == BLOCK) {  // while the first weights are on their way
+      quantize_block(quantized + KB * 64, reinterpret_cast<float*>(quantized), rend - r0, KB, a.K, tid, 64 * KS,
+                     [&](int i) {
+                       const int src = MODE == FP8_GATE_UP ? a.pairs[r0 + i] / a.k : r0 + i;
+                       return a.x + (size_t)src * a.ldx;
+                     });
+      __syncthreads();
+    }
+    if (n > 0) {
       int i = 0;
       for (; i + 2 * D <= n; i += D) {
 #pragma unroll
@@ -281,14 +330,8 @@ __global__ __launch_bounds__(64 * KS) void fp8_stream_kernel(Fp8Args a) {
   }
 }
 
-// Decoding through one matrix: up to 16 token rows, weights read once.  The
-// streaming kernel's items with the tokens quantised once per block: each wave
-// first has D steps of weights in flight, then the block quantises the rows
-// into LDS (16 lanes per 128-column block), then the steps run on codes from
-// LDS (row stride K + 16 bytes: the 16 rows of a fragment read start 4 banks
-// apart).  Bound by the latency of a launch and of one trip to memory; the
-// quantisation per wave that the streaming kernel does instead costs more than
-// the products here.
+// Decoding through one matrix: up to 16 token rows, weights read once, all rows quantised into LDS by every block.
+// Bound by the latency of a launch and of one trip to memory (1 x 7168 x 2048: 5.4 us).
 template <int R, int KS, int D>
 __global__ __launch_bounds__(64 * KS) void fp8_decode_kernel(Fp8Args a) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -316,8 +359,8 @@ __global__ __launch_bounds__(64 * KS) void fp8_decode_kernel(Fp8Args a) {
 #pragma unroll
     for (int f = 0; f < R; ++f) {
       const uint8_t* p = wrow[f] + (size_t)kb * kFp8Blk;
-      st.w[f][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + lo));
-      st.w[f][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + hi));
+      st.w[f][0] = *reinterpret_cast<const u32x4*>(p + lo);
+      st.w[f][1] = *reinterpret_cast<const u32x4*>(p + hi);
       st.s[f] = wsc[f][kb];
     }
   };
@@ -325,17 +368,7 @@ __global__ __launch_bounds__(64 * KS) void fp8_decode_kernel(Fp8Args a) {
   Step st[D];
 #pragma unroll
   for (int u = 0; u < D; ++u) load(st[u], wv + u * KS);
-  // pieces of 8 values: 16 consecutive lanes have one block of one row
-  const int pieces = a.rows * KB * 16;
-  for (int c = tid; c < pieces; c += 64 * KS) {
-    const int blk = c >> 4, row = blk / KB, kb = blk - row * KB, col = kb * kFp8Blk + 8 * (c & 15);
-    u32x4 v = {0, 0, 0, 0};
-    if (col < a.K) v = *reinterpret_cast<const u32x4*>(a.x + (size_t)row * a.ldx + col);
-    float f, s;
-    fp8_factor(max_row16(bf16x2_max(fp8_amax8(v, kFp8TinyBits))), f, s);
-    *reinterpret_cast<uint2*>(codes + row * stride + col) = fp8_codes8(v, f);
-    if ((c & 15) == 0) scales[kb * 16 + row] = s;
-  }
+  quantize_block(codes, scales, a.rows, KB, a.K, tid, 64 * KS, [&](int i) { return a.x + (size_t)i * a.ldx; });
   __syncthreads();
   f32x4 acc[R];
 #pragma unroll
@@ -396,16 +429,29 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Args a) {
   store4(a.out + (size_t)row * a.ldo, n, a.N, v);
 }
 
-template <int NT, int R, int KS, int D, Fp8Mode MODE, bool CODES>
+// Grouped token tiles of `per` rows, at most: an expert's last one need not be full.
+long long most_tiles(const Fp8Args& a, int per) {
+  return min((long long)a.rows, (long long)(a.rows + per - 1) / per + min(a.rows, a.E));
+}
+
+template <int NT, int R, int KS, int D, Fp8Mode MODE, Fp8Source SRC>
 hipError_t launch_one(const Fp8Args& a, int cus, hipStream_t s) {
   const int span = MODE == FP8_GATE_UP ? a.N / 2 : a.N, per = MODE == FP8_GATE_UP ? 8 * R : 16 * R;
   const long long slabs = (span + per - 1) / per;
-  const long long tiles = (a.rows + 16 * NT - 1) / (16 * NT) + (MODE == FP8_DENSE ? 0 : (a.rows < a.E ? a.rows : a.E));
+  const int kRows = SRC == BLOCK ? a.cap : 16 * NT;
+  const long long tiles = MODE == FP8_DENSE ? (a.rows + kRows - 1) / kRows : most_tiles(a, kRows);
   long long grid = tiles * slabs;
   // dense: a block per item; grouped (the number of items is known on the device only): as many as run at once
   if (MODE != FP8_DENSE && grid > 3LL * cus) grid = 3LL * cus;
-  const int runs = MODE == FP8_DENSE && !CODES ? a.splits : 1;
-  fp8_stream_kernel<NT, R, KS, D, MODE, CODES><<<dim3((unsigned)grid, runs), dim3(64 * KS), 0, s>>>(a);
+  const int runs = MODE == FP8_DENSE && SRC == SELF ? a.splits : 1;
+  size_t bytes = 0;
+  if constexpr (SRC == BLOCK) {
+    bytes = block_lds(a.cap, (a.K + kFp8Blk - 1) / kFp8Blk);
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&fp8_stream_kernel<NT, R, KS, D, MODE, SRC>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != hipSuccess) return e;
+  }
+  fp8_stream_kernel<NT, R, KS, D, MODE, SRC><<<dim3((unsigned)grid, runs), dim3(64 * KS), bytes, s>>>(a);
   return hipGetLastError();
 }
 
@@ -426,7 +472,14 @@ hipError_t launch_decode(const Fp8Args& a, hipStream_t s) {
 
 template <Fp8Mode MODE>
 hipError_t launch_grouped(const Fp8Args& a, int cus, hipStream_t s) {
-  return a.rows <= 16LL * a.E ? launch_one<1, 4, 4, 2, MODE, false>(a, cus, s) : launch_one<2, 4, 4, 2, MODE, false>(a, cus, s);
+  if (a.cap > 0) {
+    // items of 64 weight rows; of 32, with as many bytes in flight, while there are few (H 4096, I 1408, top-6, T = 1:
+    // 34 -> 30 us; 4 tokens of H 7168, I 256, top-8: 51 -> 59)
+    const long long slabs = MODE == FP8_GATE_UP ? (a.N / 2 + 31) / 32 : (a.N + 63) / 64;  // of 64 rows
+    return most_tiles(a, a.cap) * slabs <= 3LL * cus / 2 ? launch_one<1, 2, 4, 4, MODE, BLOCK>(a, cus, s)
+                                                         : launch_one<1, 4, 4, 2, MODE, BLOCK>(a, cus, s);
+  }
+  return a.rows <= 16LL * a.E ? launch_one<1, 4, 4, 2, MODE, SELF>(a, cus, s) : launch_one<2, 4, 4, 2, MODE, SELF>(a, cus, s);
 }
 
 }  // namespace
@@ -461,9 +514,15 @@ size_t fp8_split_bytes(int max_M, int N, int K) {
   return n;
 }
 
+// A tile holds an expert's rows of up to 16 tokens where two blocks' codes fit a CU's LDS.
+int fp8_block_rows(int T, int K) {
+  const int cap = min(T, 16);
+  return block_lds(cap, (K + kFp8Blk - 1) / kFp8Blk) <= 64 * 1024 ? cap : 0;
+}
+
 hipError_t launch_fp8_split(const Fp8Args& a, hipStream_t s) {
-  const hipError_t e = a.rows <= 16 ? launch_one<1, 1, 8, 2, FP8_DENSE, false>(a, 0, s)
-                                    : launch_one<2, 1, 8, 2, FP8_DENSE, false>(a, 0, s);
+  const hipError_t e = a.rows <= 16 ? launch_one<1, 1, 8, 2, FP8_DENSE, SELF>(a, 0, s)
+                                    : launch_one<2, 1, 8, 2, FP8_DENSE, SELF>(a, 0, s);
   if (e != hipSuccess) return e;
   const long long quads = (long long)a.rows * ((a.N + 15) / 16 * 4);
   fp8_join_kernel<<<dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s>>>(a);
@@ -476,9 +535,9 @@ hipError_t launch_fp8_stream(Fp8Mode mode, const Fp8Args& a, int cus, hipStream_
       if (!a.xq) return launch_decode<1, 8, 2>(a, s);
       // codes, up to 32 rows: 16 waves share a long K (16 x 4096 x 7168: 13.8 us, 8 waves on 32 rows of weights
       // 17.9), 8 a short one (16 x 7168 x 2048: 8.7 us against 10.8)
-      if (a.rows > 16) return launch_one<2, 1, 16, 2, FP8_DENSE, true>(a, cus, s);
-      return a.K >= 32 * kFp8Blk ? launch_one<1, 1, 16, 2, FP8_DENSE, true>(a, cus, s)
-                                 : launch_one<1, 2, 8, 2, FP8_DENSE, true>(a, cus, s);
+      if (a.rows > 16) return launch_one<2, 1, 16, 2, FP8_DENSE, CODES>(a, cus, s);
+      return a.K >= 32 * kFp8Blk ? launch_one<1, 1, 16, 2, FP8_DENSE, CODES>(a, cus, s)
+                                 : launch_one<1, 2, 8, 2, FP8_DENSE, CODES>(a, cus, s);
     case FP8_GATE_UP: return launch_grouped<FP8_GATE_UP>(a, cus, s);
     default: return launch_grouped<FP8_DOWN>(a, cus, s);
   }

@@ -322,6 +322,38 @@ def test_experts_in_the_layer(T, H, I, E, k, only, limit):
     assert torch.equal(y2[:T * k], y[:T * k])
 
 
+@pytest.mark.parametrize("T,H,I,E,k,only,limit", [
+    (1, 1024, 384, 8, 8, None, 0.0), (8, 1024, 512, 64, 6, None, 0.0), (7, 7168, 128, 4, 3, None, 0.0),
+    (2, 1152, 1152, 30, 7, None, 0.0), (5, 2176, 256, 1024, 32, None, 0.0), (8, 512, 4096, 6, 2, [2], 0.05),
+    # rows whose codes do not fit LDS: quantised by every wave, tiles of 16 and of 32 rows
+    (8, 8192, 128, 4, 2, None, 0.0), (40, 8192, 128, 2, 1, [0], 0.0),
+])
+def test_experts_of_few_tokens(T, H, I, E, k, only, limit):
+    test_experts_in_the_layer(T, H, I, E, k, only, limit)
+
+
+@pytest.mark.parametrize("T", [3, 8, 100])
+def test_experts_picked_twice_by_a_token(T):
+    """An expert may hold more rows than there are tokens."""
+    rng = np.random.default_rng(T)
+    d, (H, I, E, k) = gh.dev(), (384, 256, 5, 4)
+    x, w = _x(rng, T, H), _layer(rng, H, I, E)
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    ids[::2] = 3
+    shape = lib.make_shape(H, I, E, k, T, "bf16")
+    off = torch.empty(E + 1, dtype=torch.int32, device=d)
+    pairs, pos = (torch.empty(T * k, dtype=torch.int32, device=d) for _ in range(2))
+    xd = gh.to_device_x(x)
+    lib.moe_permute(shape, T, torch.from_numpy(ids).to(d), xd, off, pairs, pos, xd)
+    y = torch.full((T * k, H), 7.0, dtype=torch.bfloat16, device=d)
+    ws = torch.full((lib.moe_fp8_experts_workspace_bytes(shape),), 0xFF, dtype=torch.uint8, device=d)
+    lib.moe_fp8_experts(shape, T, *(torch.from_numpy(v).to(d) for v in w), off, pairs, xd, y, ws)
+    torch.cuda.synchronize()
+    ref = fb.experts(x, ids, *w, 0.0)
+    got = y.double().cpu().numpy()
+    assert np.linalg.norm(got - ref) <= 6e-3 * np.linalg.norm(ref)
+
+
 @pytest.mark.parametrize("T", [5, 600])
 def test_experts_captured_and_shared_workspace(T):
     """Two layers captured into graphs that share one workspace, replayed in turn beside eager calls."""
