@@ -32,6 +32,8 @@ constexpr float kFp8Tiny = 7.8886090522101181e-31f;  // 2^-100: smallest magnitu
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 enum Fp8Mode { FP8_DENSE = 0, FP8_GATE_UP = 1, FP8_DOWN = 2 };
 
@@ -166,6 +168,35 @@ __device__ __forceinline__ float swiglu(float g, float u, float limit) {
 __device__ __forceinline__ f32x4 fp8_mfma(const i32x8& a, const i32x8& b) {
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
+}
+
+// The same product from the codes as bf16 values (exact, and so are their products): four instructions, each of 8 of a
+// lane's 32 values.
+struct Bf16Frag {
+  bf16x8 v[4];
+};
+__device__ __forceinline__ Bf16Frag bf16_frag(const i32x8& c) {
+  Bf16Frag o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    union {
+      bf16x2 p[4];
+      bf16x8 v;
+    } u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      u.p[2 * i] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * j + i], 1.f, false);
+      u.p[2 * i + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * j + i], 1.f, true);
+    }
+    o.v[j] = u.v;
+  }
+  return o;
+}
+__device__ __forceinline__ f32x4 bf16_mfma(const Bf16Frag& a, const Bf16Frag& b) {
+  f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[j], b.v[j], z, 0, 0, 0);
+  return z;
 }
 
 // ------------------------------------------------------------------ launchers

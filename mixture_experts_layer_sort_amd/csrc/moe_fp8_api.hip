@@ -177,12 +177,12 @@ moe_status moe_fp8_experts(const moe_shape* s, int32_t T, const void* w13_codes,
   a.rows = T * s->top_k, a.E = s->num_experts, a.N = 2 * s->inter, a.K = s->hidden, a.k = s->top_k;
   a.limit = s->gate_up_limit;
   hipError_t e;
-  // The tiled kernel; the streaming one for up to 8 tokens (H 7168, I 2048, 256 experts, top-8, T = 4: 248 us against
-  // 258; H 4096, I 1408, 64 experts, top-6, T = 8: 132 against 146; at T = 16 and uneven experts 102 against 77), where
-  // the tiles (128 intermediate columns each) would leave half of the compute units idle, and for gathered rows beyond
-  // the tiled kernel's 32-bit addresses.
+  // The tiled kernel; the streaming one for up to 8 tokens of 48 rows (H 4096, I 1408, 64 experts, top-6, T = 8: 125 us
+  // against 146; H 7168, I 2048, 256 experts, top-8, T = 4: 254 against 258, T = 8: 460 against 413; at T = 16 and uneven
+  // experts 102 against 77), where the tiles (128 intermediate columns each) would leave half of the compute units idle,
+  // and for gathered rows beyond the tiled kernel's 32-bit addresses.
   const long long P = (long long)T * s->top_k;
-  if (T > 8 && P * (s->inter / 128) > cus / 2 && (long long)T * s->hidden < (1LL << 31)) {
+  if ((T > 8 || P > 48) && P * (s->inter / 128) > cus / 2 && (long long)T * s->hidden < (1LL << 31)) {
     const int tile = fp8_tile_tokens(P, s->num_experts);
     const long long ntok = (long long)max_tiles(s, P, tile);
     float* xs = (float*)(base + W.xs);
