@@ -512,6 +512,7 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 // One block does it all while its 16 waves have two batches of four tokens at most, and their records fit LDS (40 tokens
 // of 24 sequences, 64 experts: 8.5 us against 15.4; 500 tokens: 15.1 against 11.0).
+constexpr int kSmallLds = 128 * 1024;
 size_t small_lds(const BalanceArgs& a) {
   const size_t slots = 16 + a.S, slices = (a.E + 63) / 64;
   return a.S * (slices + 1) * 8 + slots * 8 + slots * a.E * 8;
@@ -519,12 +520,12 @@ size_t small_lds(const BalanceArgs& a) {
 
 hipError_t launch_balance_loss(const BalanceArgs& a, uint8_t* ws, hipStream_t s) {
   const bool vec = a.E % 4 == 0 && a.E > 128 && aligned16(a.logits);
-  if (a.T <= 128 && small_lds(a) <= 128 * 1024) {
+  if (a.T <= 128 && small_lds(a) <= kSmallLds) {
     const int bytes = (int)small_lds(a), chunk = (a.T + 15) / 16;
     return dispatch(a, vec, [&](auto v, auto n) {
       const hipError_t e = hipFuncSetAttribute(
           reinterpret_cast<const void*>(&balance_small_kernel<decltype(v)::value, decltype(n)::value>),
-          hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+          hipFuncAttributeMaxDynamicSharedMemorySize, kSmallLds);
       if (e != hipSuccess) return e;
       balance_small_kernel<decltype(v)::value, decltype(n)::value><<<dim3(1), dim3(1024), bytes, s>>>(a, chunk);
       return hipGetLastError();

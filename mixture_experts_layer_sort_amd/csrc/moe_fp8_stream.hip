@@ -36,6 +36,9 @@ __device__ __forceinline__ void store4(uint16_t* row, int n, int N, const f32x4&
 // block_lds()): the waves' steps are then little more than loads and products (T = 1 experts: 84 -> 77 us).
 enum Fp8Source { SELF, CODES, BLOCK };
 
+// Dynamic LDS of the kernels that quantise into it, at most: the limit asked for on every call (the same number, whatever
+// other threads launch meanwhile).  fp8_decode_fits() and fp8_block_rows() stay below it.
+constexpr int kBlockLds = 64 * 1024;
 __host__ __device__ inline size_t block_lds(int rows, int KB) { return (size_t)KB * 64 + (size_t)rows * (KB * kFp8Blk + 16); }
 
 // Rows `row(i)`, i < rows, of K bf16 values: codes [rows][KB 128 + 16] (row stride K + 16 bytes: the 16 rows of a fragment
@@ -455,7 +458,7 @@ hipError_t launch_one(const Fp8Args& a, int cus, hipStream_t s) {
   if constexpr (SRC == BLOCK) {
     bytes = block_lds(a.cap, (a.K + kFp8Blk - 1) / kFp8Blk);
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&fp8_stream_kernel<NT, R, KS, D, MODE, SRC>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kBlockLds);
     if (e != hipSuccess) return e;
   }
   fp8_stream_kernel<NT, R, KS, D, MODE, SRC><<<dim3((unsigned)grid, runs), dim3(64 * KS), bytes, s>>>(a);
@@ -471,7 +474,7 @@ template <int R, int KS, int D>
 hipError_t launch_decode(const Fp8Args& a, hipStream_t s) {
   const size_t bytes = decode_lds<R, KS>(a.rows, a.K);
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&fp8_decode_kernel<R, KS, D>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, kBlockLds);
   if (e != hipSuccess) return e;
   fp8_decode_kernel<R, KS, D><<<dim3((a.N + 16 * R - 1) / (16 * R)), dim3(64 * KS), bytes, s>>>(a);
   return hipGetLastError();
@@ -526,7 +529,7 @@ size_t fp8_split_bytes(int max_M, int N, int K) {
 // A tile holds an expert's rows of up to 16 tokens where two blocks' codes fit a CU's LDS.
 int fp8_block_rows(int T, int K) {
   const int cap = min(T, 16);
-  return block_lds(cap, (K + kFp8Blk - 1) / kFp8Blk) <= 64 * 1024 ? cap : 0;
+  return block_lds(cap, (K + kFp8Blk - 1) / kFp8Blk) <= kBlockLds ? cap : 0;
 }
 
 hipError_t launch_fp8_split(const Fp8Args& a, hipStream_t s) {

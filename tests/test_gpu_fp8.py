@@ -178,6 +178,42 @@ def test_linear_special_values(M):
     _check(got[:, keep], ref[:, keep], groups[:, keep])
 
 
+@pytest.mark.parametrize("M", [4, 20])
+def test_linear_runs_of_k_special_values_and_captured(M):
+    """K split over blocks: infinities and NaN in any run spoil their own row only; replays give the eager bits."""
+    rng, d = np.random.default_rng(16), gh.dev()
+    N, K = 100, 4112
+    x, (c, s) = _x(rng, M, K), _weights(rng, N, K)
+    xf = codecs.bf16_decode(x).copy()
+    xf[0] = 0.0
+    x = codecs.bf16_encode(xf.astype(np.float32))
+    ref, groups = fb.linear(x, c, s)
+    keep = np.arange(M) != 3
+    for bad, col in ((np.inf, 0), (-np.inf, 2047), (np.nan, 4111)):
+        xt = torch.from_numpy(x.view(np.int16)).view(torch.bfloat16).clone()
+        xt[3, col] = bad
+        got, _ = _linear(xt.view(torch.int16).numpy().view(np.uint16), c, s)
+        assert np.isnan(got[3]).all() and not got[0].any()
+        _check(got[keep], ref[keep], groups[keep])
+    cd, sd, xd = torch.from_numpy(c).to(d), torch.from_numpy(s).to(d), gh.to_device_x(x)
+    ws = torch.empty(lib.moe_fp8_linear_workspace_bytes(M, N, K), dtype=torch.uint8, device=d)
+    out, eager = (torch.empty(M, N, dtype=torch.bfloat16, device=d) for _ in range(2))
+    lib.moe_fp8_linear(M, N, K, cd, sd, xd, out, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lib.moe_fp8_linear(M, N, K, cd, sd, xd, out, ws)
+    for i in range(4):
+        xd.mul_(-1.0 if i % 2 else 0.5)
+        out.zero_()
+        ws.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        lib.moe_fp8_linear(M, N, K, cd, sd, xd, eager, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), i
+
+
 @pytest.mark.parametrize("M", [2, 20, 70])
 def test_linear_offsets_beyond_32_bits(M):
     """A weight matrix of over 2^31 codes, and rows of x and out over 2^32 elements apart in all: the first and the last
@@ -352,6 +388,32 @@ def test_experts_picked_twice_by_a_token(T):
     ref = fb.experts(x, ids, *w, 0.0)
     got = y.double().cpu().numpy()
     assert np.linalg.norm(got - ref) <= 6e-3 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("T", [3, 40, 400])
+def test_experts_of_a_token_that_is_not_finite(T):
+    """NaN in every row of that token, nothing in the others (which share experts, tiles and blocks with it)."""
+    rng = np.random.default_rng(T)
+    d, (H, I, E, k) = gh.dev(), (512, 256, 4, 2)
+    w = [torch.from_numpy(v).to(d) for v in _layer(rng, H, I, E)]
+    ids = torch.from_numpy(np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32)).to(d)
+    shape = lib.make_shape(H, I, E, k, T, "bf16")
+    off = torch.empty(E + 1, dtype=torch.int32, device=d)
+    pairs, pos = (torch.empty(T * k, dtype=torch.int32, device=d) for _ in range(2))
+    ws = torch.full((lib.moe_fp8_experts_workspace_bytes(shape),), 0xFF, dtype=torch.uint8, device=d)
+    x = gh.to_device_x(_x(rng, T, H))
+    lib.moe_permute(shape, T, ids, x, off, pairs, pos, x)
+    ys = []
+    for bad in (0.0, float("nan"), float("inf")):
+        x[1, 200] = bad
+        y = torch.empty(T * k, H, dtype=torch.bfloat16, device=d)
+        lib.moe_fp8_experts(shape, T, *w, off, pairs, x, y, ws)
+        torch.cuda.synchronize()
+        ys.append(y.view(T, k, H))
+    rest = torch.arange(T, device=d) != 1
+    assert bool(torch.isfinite(ys[0]).all())
+    for y in ys[1:]:
+        assert bool(torch.isnan(y[1]).all()) and torch.equal(y[rest], ys[0][rest])
 
 
 @pytest.mark.parametrize("T", [5, 600])

@@ -193,6 +193,24 @@ def test_tokens_in_no_sequence():
     assert np.all(np.abs(g - ref) <= TOL * mag)
 
 
+@pytest.mark.parametrize("T", [128, 129, 3000])
+def test_tokens_outside_of_many_sequences(T):
+    """Empty sequences, some of one token, tokens before the first and behind the last, around the sizes where the
+    number of launches changes."""
+    rng, logits, ids, _, mask = _case(T, 60, 3, 1, True, 17)
+    off = np.array([5, 5, 6, 7, 7, T // 2, T // 2 + 1, T - 20, T - 20], np.int32)
+    loss, counts, tokens = _loss(logits, ids, off, mask, 0.5, 0.25)
+    rl, rc, rt = router.balance_loss(logits, ids, 0.5, 0.25, mask, off)
+    assert np.array_equal(counts.cpu().numpy(), rc) and np.array_equal(tokens.cpu().numpy(), rt)
+    assert np.all(np.abs(loss.double().cpu().numpy() - rl) <= TOL * np.abs(rl))
+    again = _loss(logits, ids, off, mask, 0.5, 0.25)
+    assert torch.equal(again[0], loss)
+    w, dw = rng.random(ids.shape).astype(np.float32), rng.standard_normal(ids.shape).astype(np.float32)
+    ref, mag = router.backward(logits, ids, w, dw, (1.0, 1.0), 0.5, 0.25, mask, off)
+    g = _grad(logits, ids, off, mask, 0.5, 0.25, w, dw, np.ones(2, np.float32), counts, tokens)
+    assert np.all(np.abs(g - ref) <= TOL * mag)
+
+
 def test_unaligned_rows_and_one_sequence_without_offsets():
     """Logits and gradients that begin 4 bytes into an allocation (no 16-byte rows), offsets left out."""
     rng, logits, ids, off, _ = _case(37, 256, 8, 1, False, 8)
