@@ -28,8 +28,8 @@
 //   start(kb): X(kb) has landed, everyone is done with stage kb - 1; Y(kb + 1) is issued
 //   mid(kb):   Y(kb) has landed, everyone is done with X(kb);        X(kb + 2) is issued
 //
-// Measured: 8192 x 4096 x 7168 in 200 us (2.4 PFLOP/s; 231 with the quantiser); 500 x 2816 x 4096 in 15 us; experts of
-// 8192 tokens (256 experts, top-8, H 7168, I 2048) 2.6 ms gate / up and 1.4 ms down (1.4 PFLOP/s: the tiles are two
+// Measured: 8192 x 4096 x 7168 in 208 us (2.3 PFLOP/s; 231 with the quantiser); 500 x 2816 x 4096 in 17 us; experts of
+// 8192 tokens (256 experts, top-8, H 7168, I 2048) 2.6 ms gate / up and 1.5 ms down (1.4 PFLOP/s: the tiles are two
 // thirds full); of 333 tokens (64 experts, top-6, H 4096, I 1408) 272 us, 4.1 TB/s of weights.
 #include "moe_fp8.h"
 
