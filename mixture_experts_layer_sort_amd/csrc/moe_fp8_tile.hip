@@ -449,19 +449,29 @@ __global__ __launch_bounds__(64 * S::NW * S::KG) void fp8_tile_kernel(Fp8Args a,
       }
     }
     wait_barrier<0>();
-    const bool vec = a.ldo % 8 == 0 && ((uintptr_t)a.out & 15) == 0;
-    for (int c = tid; c < S::BT * kPieces; c += 64 * S::NW * S::KG) {
-      const int tok = c / kPieces, p = c % kPieces, n = n0 + 8 * p;
-      if (r0 + tok >= rend || n >= a.N) continue;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(lds + tok * (S::BN * 2) + ((p ^ (tok & (kPieces - 1))) << 4));
-      const size_t row = MODE == FP8_DOWN ? (size_t)a.pairs[r0 + tok] : (size_t)(r0 + tok);
-      uint16_t* out = a.out + row * (size_t)a.ldo + n;
-      if (vec && n + 8 <= a.N) {
-        *reinterpret_cast<u32x4*>(out) = v;
-      } else {
+    auto out_row = [&](int tok) {
+      return a.out + (MODE == FP8_DOWN ? (size_t)a.pairs[r0 + tok] : (size_t)(r0 + tok)) * (size_t)a.ldo;
+    };
+    if (a.ldo % 8 == 0 && ((uintptr_t)a.out & 15) == 0) {
+      for (int c = tid; c < S::BT * kPieces; c += 64 * S::NW * S::KG) {
+        const int tok = c / kPieces, p = c % kPieces, n = n0 + 8 * p;
+        if (r0 + tok >= rend || n >= a.N) continue;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(lds + tok * (S::BN * 2) + ((p ^ (tok & (kPieces - 1))) << 4));
+        uint16_t* out = out_row(tok) + n;
+        if (n + 8 <= a.N) {
+          *reinterpret_cast<u32x4*>(out) = v;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (n + i < a.N) out[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+          for (int i = 0; i < 8; ++i)
+            if (n + i < a.N) out[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+        }
+      }
+    } else {  // rows at any alignment: a value per lane, so that a wave's lanes write one run (5570 x 3551 x 144: 57
+      for (int c = tid; c < S::BT * S::BN; c += 64 * S::NW * S::KG) {  // -> 45 us; 3552 columns: 28)
+        const int tok = c / S::BN, col = c % S::BN;
+        if (r0 + tok >= rend || n0 + col >= a.N) continue;
+        out_row(tok)[n0 + col] = *reinterpret_cast<const uint16_t*>(
+            lds + tok * (S::BN * 2) + (((col >> 3) ^ (tok & (kPieces - 1))) << 4) + (col & 7) * 2);
       }
     }
   }
