@@ -52,17 +52,17 @@ struct TileShape {
   static_assert(TF == 8 || TF == 4, "a half's scales fit a wave");
 };
 
-// Direct global->LDS loads of 16 and 4 bytes per lane, at base + off + soff (soff: the same for all lanes).  `bytes`
-// from base on are inside the buffer: a lane whose address lies behind them reads nothing (rows past the end of a
-// tile; their results are dropped).
+// Direct global->LDS loads of 16 and 4 bytes per lane, at base + off.  `bytes` from base on are inside the buffer: a
+// lane with off >= bytes reads nothing (rows past the end of a tile; their results are dropped).  The range check is
+// promised for the lane's own offset only, not for the instruction's scalar one, so that one stays 0.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
 }
-__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff, void* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, soff, 0, 0);
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, uint32_t off, void* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
 }
-__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff, void* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, off, soff, 0, 0);
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, uint32_t off, void* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, off, 0, 0, 0);
 }
 
 // Wait until at most N of this wave's vector-memory operations are
@@ -126,17 +126,18 @@ __global__ __launch_bounds__(64 * S::NW * S::KG) void fp8_tile_kernel(Fp8Args a,
   const int frags = (min(rend - r0, S::BT) + 15) >> 4;
   const int live = (frags - wt + S::WT - 1) / S::WT;
 
-  // Loads.  This lane's part of an instruction: 8 rows of 8 pieces, row lane / 8, slot lane % 8.  Rows are
-  // consecutive, so one lane offset serves all instructions and the rest is scalar; only the gathered rows of
-  // GATE_UP (xq through the pairs) have offsets of their own.
+  // Loads.  This lane's part of an instruction: 8 rows of 8 pieces, row lane / 8, slot lane % 8.  Each load of a step
+  // has its lane offsets in a register; the K block is in the buffer's base, made once a step.  (Offsets added up per
+  // load: 8192 x 4096 x 7168 7 % slower.)
   const int lrow = lane >> 3, piece = (lane & 7) ^ lrow;
   // first token row of load j: half of each wave's loads fill the first half of the tile's tokens
   auto tok_row = [&](int j) { return j / (S::LB / 2) * (S::BT / 2) + 8 * (wv * (S::LB / 2) + j % (S::LB / 2)); };
   // A wave loads the scales of its own tokens: lane l that of fragment (h TF / 2 + l / 16), token l % 16, of half h
   // (TF = 4 needs 32 of them; the other lanes repeat them into slots of their own)
   auto scale_row = [&](int h) { return 16 * ((h * (S::TF / 2) + (lane >> 4) % (S::TF / 2)) * S::WT + wt) + (lane & 15); };
-  const uint32_t wrow = (uint32_t)lrow * (uint32_t)a.K;
-  uint32_t xoff[MODE == FP8_GATE_UP ? S::LB : 1], soff[MODE == FP8_GATE_UP ? 2 : 1];
+  uint32_t woff[S::LA], xoff[S::LB], soff[2];
+#pragma unroll
+  for (int i = 0; i < S::LA; ++i) woff[i] = (uint32_t)(8 * i + lrow) * (uint32_t)a.K + 16 * piece;
   if constexpr (MODE == FP8_GATE_UP) {
 #pragma unroll
     for (int j = 0; j < S::LB; ++j)
@@ -147,8 +148,10 @@ __global__ __launch_bounds__(64 * S::NW * S::KG) void fp8_tile_kernel(Fp8Args a,
     for (int h = 0; h < 2; ++h)
       soff[h] = 4u * (uint32_t)(a.pairs[min(r0 + scale_row(h), rend - 1)] / a.k);
   } else {
-    xoff[0] = (uint32_t)lrow * (uint32_t)Kp + 16 * piece;
-    soff[0] = 4 * scale_row(0);
+#pragma unroll
+    for (int j = 0; j < S::LB; ++j) xoff[j] = (uint32_t)(tok_row(j) + lrow) * (uint32_t)Kp + 16 * piece;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) soff[h] = 4 * scale_row(h);
   }
   // this wave's weight rows of the tile: 8 LA from row 8 LA wv on (GATE_UP: all gate rows or all up rows)
   const int wfirst = 8 * S::LA * wv;
@@ -158,34 +161,25 @@ __global__ __launch_bounds__(64 * S::NW * S::KG) void fp8_tile_kernel(Fp8Args a,
   const int wbytes = min(a.N - wn, 8 * S::LA) * a.K;  // may be negative: no rows
   const uint8_t* xbase = MODE == FP8_GATE_UP ? a.xq : a.xq + (size_t)r0 * Kp;
   const float* sbase = MODE == FP8_GATE_UP ? a.xs : a.xs + r0;
-  const int xrows = min(rend - r0, S::BT);
+  const int xrows = MODE == FP8_GATE_UP ? a.xrows : min(rend - r0, S::BT);
   // The loads of one step, one by one (X: LA of weights, LB / 2 of tokens, 1 of scales; Y: LB / 2 and 1).  Steps past
   // the last one load the last one again (into a stage that is not read any more), so that the counts of the waits
   // hold to the end.
   auto stage = [&](int step) { return lds + (S::kTwo ? step & 1 : step % S::NS) * S::kStage; };
   auto load_tokens = [&](int step, int j) {
-    const int kb = min(step * S::KG + kg, KB - 1), row = tok_row(j);
-    uint8_t* to = stage(step) + S::kA + row * 128;
-    if constexpr (MODE == FP8_GATE_UP)
-      load_lds16(rsrc_of(xbase + kb * kFp8Blk, 0x7FFFFFFF), xoff[j], 0, to);
-    else
-      load_lds16(rsrc_of(xbase + kb * kFp8Blk, (xrows * Kp - kb * kFp8Blk)), xoff[0], row * Kp, to);
+    const int kb = min(step * S::KG + kg, KB - 1);
+    load_lds16(rsrc_of(xbase + kb * kFp8Blk, xrows * Kp - kb * kFp8Blk), xoff[j], stage(step) + S::kA + tok_row(j) * 128);
   };
   auto load_scales = [&](int step, int h) {
     const int kb = min(step * S::KG + kg, KB - 1);
-    uint8_t* to = stage(step) + S::kA + S::kB + (wv * 2 + h) * 256;
-    if constexpr (MODE == FP8_GATE_UP)
-      load_lds4(rsrc_of(sbase + (size_t)kb * a.xrows, 0x7FFFFFFF), soff[h], 0, to);
-    else
-      load_lds4(rsrc_of(sbase + (size_t)kb * a.xrows, (xrows * 4)), soff[0], h * (S::BT / 2) * 4, to);
+    load_lds4(rsrc_of(sbase + (size_t)kb * a.xrows, xrows * 4), soff[h], stage(step) + S::kA + S::kB + (wv * 2 + h) * 256);
   };
   auto issue_x = [&](int step, int i) {
     if (i < S::LA) {
       const int kb = min(step * S::KG + kg, KB - 1);
-      // pieces past the end of a weight row (K not a multiple of 128) load the block's first piece; they are
-      // cleared in the fragments
-      const uint32_t woff = wrow + (kb * kFp8Blk + 16 * piece < a.K ? 16u * piece : 0u);
-      load_lds16(rsrc_of(wbase + kb * kFp8Blk, max(wbytes - kb * kFp8Blk, 0)), woff, 8 * i * a.K,
+      // pieces past the end of a weight row (K not a multiple of 128) load from the next row, or lie behind the buffer's
+      // end; they are cleared in the fragments
+      load_lds16(rsrc_of(wbase + kb * kFp8Blk, max(wbytes - kb * kFp8Blk, 0)), woff[i],
                  stage(step) + (wfirst + 8 * i) * 128);
     } else if (i < S::LA + S::LB / 2) {
       load_tokens(step, i - S::LA);
