@@ -352,7 +352,7 @@ MOE_API moe_status moe_fp8_linear(int32_t M, int32_t N, int32_t K, const void* c
 /* The expert MLPs of routed tokens on such weights: for sorted row r of expert
  * e, p = sorted_pairs[r], t = p / top_k:
  *   g, u = W13[e] . quant(x[t]) (rows [0, I) gate, [I, 2I) up; the shape's
- *   gate_up_limit as in moe_gemm13_swiglu_quant), h = bf16(silu(g) * u),
+ *   gate_up_limit as in moe_gemm13_swiglu_quant, a NaN stays one), h = bf16(silu(g) * u),
  *   y[p] = bf16( W2[e] . quant(h) ).
  * offsets [E + 1] and sorted_pairs [T top_k] are moe_permute's outputs, x is
  * bf16 [T, H], y bf16 [T top_k, H] (moe_combine's input): moe_route,

@@ -158,9 +158,9 @@ __device__ __forceinline__ uint2 fp8_codes8(const u32x4& v, float f) {
 }
 
 __device__ __forceinline__ float swiglu(float g, float u, float limit) {
-  if (limit > 0.f) {
-    g = fminf(g, limit);
-    u = fminf(fmaxf(u, -limit), limit);
+  if (limit > 0.f) {  // by comparisons, which leave a NaN as it is
+    g = g > limit ? limit : g;
+    u = u > limit ? limit : u < -limit ? -limit : u;
   }
   return g / (1.f + __expf(-g)) * u;
 }
