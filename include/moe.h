@@ -384,8 +384,9 @@ MOE_API moe_status moe_fp8_experts(const moe_shape* shape, int32_t T, const void
  * (n_s).  The results do not depend on scheduling.  1 <= E <= 1024, 1 <= k <=
  * min(E, 32), T k <= 2^24, num_seqs <= 65536 (else MOE_ERR_UNSUPPORTED); T == 0
  * is a no-op.  ws: moe_balance_loss_workspace_bytes(T, E, num_seqs) bytes (0
- * for unsupported arguments), aligned to 256; need not be cleared, and calls
- * that share it must be stream-ordered. */
+ * for unsupported arguments; the bytes for a batch serve any with at most as
+ * many tokens, experts and sequences), aligned to 256; need not be cleared, and
+ * calls that share it must be stream-ordered. */
 MOE_API size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t E, int32_t num_seqs);
 MOE_API moe_status moe_balance_loss(int32_t T, int32_t E, int32_t k, const float* logits, const int32_t* topk_ids,
                                     const uint8_t* token_mask, int32_t num_seqs, const int32_t* seq_offsets,

@@ -25,7 +25,8 @@ struct BalanceArgs {
   float* d_logits;             // [T, E]
 };
 
-// Workspace of the forward pass (bytes into it).
+// Workspace of the forward pass (bytes into it).  Its size grows with T, E and S, so that of the largest batch serves
+// all: records for the most chunks that T tokens or fewer can have (the number itself falls where the chunks grow).
 struct BalanceWorkspace {
   size_t prob, count, zn, part, ticket, total;
 };
@@ -42,7 +43,8 @@ inline int balance_slices(int E) { return (E + kBalanceSlice - 1) / kBalanceSlic
 
 inline BalanceWorkspace balance_workspace(int T, int E, int S) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  const size_t slots = (size_t)balance_chunks(T) + S;
+  const size_t most = ((size_t)T + 4 * kBalanceWaves - 1) / (4 * kBalanceWaves);
+  const size_t slots = (most < kBalanceChunks ? most : kBalanceChunks) + S;
   BalanceWorkspace w;
   w.prob = 0;
   w.count = w.prob + up(slots * E * 4);

@@ -116,3 +116,16 @@ def test_router_refusals_of_one_side():
     f = lib.moe_balance_loss_workspace_bytes
     assert f(0, 8, 1) == 0 and f(4, 1025, 1) == 0 and f(4, 8, 0) == 0 and f(4, 8, 1) > 0
     assert f((1 << 24) + 1, 8, 1) == 0 and f(4, 8, 65537) == 0
+
+
+def test_workspace_of_a_large_batch_serves_smaller_ones():
+    """Sizes never fall as a batch grows: across 16384 tokens, where chunks begin to grow, and at each later step."""
+    f = lib.moe_balance_loss_workspace_bytes
+    tokens = sorted({t + d for t in (1, 16, 128, 1000, *range(16384, 70000, 1024), 1 << 20, 1 << 24) for d in (-1, 0, 1)})
+    tokens = [t for t in tokens if 1 <= t <= 1 << 24]
+    for E, S in ((1, 1), (256, 16), (1024, 40)):
+        sizes = [f(t, E, S) for t in tokens]
+        assert sizes == sorted(sizes), (E, S)
+    assert f(5000, 64, 1) <= f(5000, 64, 2) <= f(5000, 64, 1000) <= f(5000, 64, 65536)
+    assert f(5000, 1, 3) <= f(5000, 64, 3) <= f(5000, 65, 3) <= f(5000, 1024, 3)
+    assert balance(T=16384, E=256, S=16, seq=A, nbytes=f(16384, 256, 16) - 1) == WORKSPACE
