@@ -378,7 +378,7 @@ MOE_API moe_status moe_fp8_experts(const moe_shape* shape, int32_t T, const void
  *   loss[0] = balance_coef / num_seqs * sum_s sum_e (E c_{s,e} / (k n_s)) (mean_t p_{t,e})
  *   loss[1] = z_coef / num_seqs * sum_s mean_t (log sum_e exp(logits_{t,e}))^2  (0 where z_coef == 0)
  * A sequence without valid tokens counts as 0; tokens in no sequence and masked
- * tokens have no part (whatever a masked token's logits are).  Logits may be
+ * tokens have no part (whatever their logits are).  Logits may be
  * -inf (an expert that is switched off), but not a whole row of them.
  * Outputs: loss fp32 [2], counts int32 [num_seqs, E], tokens int32 [num_seqs]
  * (n_s).  The results do not depend on scheduling.  1 <= E <= 1024, 1 <= k <=
@@ -401,7 +401,8 @@ MOE_API moe_status moe_balance_loss(int32_t T, int32_t E, int32_t k, const float
  *     counts and tokens as moe_balance_loss wrote them for the same batch
  *     (counts are constants of the gradient); NULL: none.
  * At least one of the two is given.  A masked token's row is zero, whatever
- * its inputs hold.  d_logits must not overlap the inputs.  Limits as
+ * its inputs hold; that of a token in no sequence has the weights' part alone,
+ * whatever its logits are.  d_logits must not overlap the inputs.  Limits as
  * above; no workspace. */
 MOE_API moe_status moe_route_backward(int32_t T, int32_t E, int32_t k, const float* logits, const int32_t* topk_ids,
                                       const float* topk_w, const float* d_topk_w, const uint8_t* token_mask,

@@ -365,6 +365,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(BalanceArgs a, int 
   float* rows = lds + wv * 4 * kRow;
   const float g0 = a.d_loss ? a.d_loss[0] * a.coef : 0.f, g1 = a.d_loss ? a.d_loss[1] * a.z_coef : 0.f;
   int s = -2, end = t0;  // sequence of the current token; its end
+  bool in = false;       // the token is in a sequence: the losses have a part (never without d_loss)
   float A[NC][VEC], Z = 0.f;
 #pragma unroll
   for (int i = 0; i < NC; ++i)
@@ -374,7 +375,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(BalanceArgs a, int 
   for (int tb = t0; tb < t1;) {
     if (a.d_loss && tb >= end) {
       s = seq_of(a, tb);
-      const bool in = s >= 0 && s < a.S;
+      in = s >= 0 && s < a.S;
       end = in ? seq_bound(a, s + 1) : s < 0 ? seq_bound(a, 0) : a.T;
       const float n = in ? (float)max(1, a.tokens[s]) : 1.f;
       const float sc = g0 / ((float)a.S * (float)a.k * n * n);
@@ -415,7 +416,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(BalanceArgs a, int 
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (!a.d_loss || keep[u] == 0.f) {  // whatever the row holds
+      if (!in || keep[u] == 0.f) {  // whatever the row holds
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll

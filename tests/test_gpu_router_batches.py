@@ -28,3 +28,24 @@ def test_workspace_of_the_largest_batch():
         rl, rc, rt = router.balance_loss(logits, ids, 0.01, 0.001, None, off)
         assert np.array_equal(counts.cpu().numpy(), rc) and np.array_equal(tokens.cpu().numpy(), rt)
         assert np.all(np.abs(loss.double().cpu().numpy() - rl) <= tr.TOL * np.abs(rl))
+
+
+@pytest.mark.parametrize("T", [50, 700])
+def test_rows_in_no_sequence_have_no_part(T):
+    """Rows before the first sequence and behind the last one, which hold anything: nothing reaches the losses, and
+    their gradient is that through the weights alone."""
+    rng, logits, ids, _, _ = tr._case(T, 200, 4, 1, False, 22)
+    off = np.array([9, 9, 30, T - 11], np.int32)
+    out = np.r_[0:9, T - 11:T]
+    w, dw = rng.random(ids.shape).astype(np.float32), rng.standard_normal(ids.shape).astype(np.float32)
+    dl = np.array([1.0, -0.5], np.float32)
+    a = tr._loss(logits, ids, off, None, 0.5, 0.25)
+    ga = tr._grad(logits, ids, off, None, 0.5, 0.25, w, dw, dl, a[1], a[2])
+    la = tr._grad(logits, ids, off, None, 0.5, 0.25, None, None, dl, a[1], a[2])
+    assert not la[out].any()
+    for bad in (np.nan, np.inf, -np.inf, np.finfo(np.float32).max):
+        logits[out] = bad
+        b = tr._loss(logits, ids, off, None, 0.5, 0.25)
+        assert all(torch.equal(x, y) for x, y in zip(a, b)), bad
+        assert np.array_equal(ga, tr._grad(logits, ids, off, None, 0.5, 0.25, w, dw, dl, a[1], a[2])), bad
+        assert np.array_equal(la, tr._grad(logits, ids, off, None, 0.5, 0.25, None, None, dl, a[1], a[2])), bad
