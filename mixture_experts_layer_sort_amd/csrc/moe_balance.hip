@@ -31,6 +31,14 @@
 namespace moe {
 namespace {
 
+// Between LDS accesses of one wave's lanes to each other's places.  The hardware does a wave's LDS operations in order;
+// this keeps the compiler from moving or forwarding a lane's own accesses across.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Row values of one lane: v[i][j] = row[(64 i + lane) VEC + j], `fill` past E.
 template <int VEC, int NC>
 __device__ __forceinline__ void load_row(float (&v)[NC][VEC], const float* row, int E, int lane, float fill) {
@@ -296,6 +304,7 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(BalanceArgs a, int 
   each_sequence(a, t0, min(a.T, t0 + chunk), [&](int s, int lo, int hi) {
     const int slot = wv + s;
     for (int e = lane; e < a.E; e += 64) count[slot * a.E + e] = 0;  // slots of one wave: no barrier
+    wave_sync();
     add_picks(a, lo, hi, count + slot * a.E, lane, 64);
     float acc[NC][VEC], z;
     int n;
@@ -456,6 +465,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(BalanceArgs a, int 
         for (int i = 0; i < NC; ++i)
 #pragma unroll
           for (int j = 0; j < VEC; ++j) rows[u * kRow + (64 * i + lane) * VEC + j] = v[u][i][j];
+      wave_sync();
       float x = wt[0] * dw[0] + wt[1] * dw[1];
       x += row_ror<8>(x);
       x += row_ror<4>(x);
@@ -464,6 +474,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(BalanceArgs a, int 
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if ((unsigned)id[h] < (unsigned)a.E) atomicAdd(&rows[mine * kRow + id[h]], wt[h] * (dw[h] - x));
+      wave_sync();
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll

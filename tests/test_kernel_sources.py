@@ -40,3 +40,29 @@ def test_range_checked_buffer_loads_have_no_scalar_offset():
             assert a[4] == "0", (name, a)
             seen += 1
     assert seen
+
+
+def _body(text, name):
+    """The body of the function `name`."""
+    at = text.index("{", text.index(name + "("))
+    depth, end = 1, at + 1
+    while depth:
+        depth += (text[end] == "{") - (text[end] == "}")
+        end += 1
+    return text[at:end]
+
+
+def test_lanes_that_share_lds_are_ordered():
+    """Where lanes of one wave write, add to and read each other's places in LDS, a fence of the wave stands between:
+    each lane's own accesses alone would let the compiler move or forward them."""
+    text = dict(_sources())["moe_balance.hip"]
+    sync = r"wave_sync\(\);"
+    assert re.search(r"__builtin_amdgcn_fence\(__ATOMIC_RELEASE, \"wavefront\"\);\s*__builtin_amdgcn_wave_barrier\(\);\s*"
+                     r"__builtin_amdgcn_fence\(__ATOMIC_ACQUIRE, \"wavefront\"\);", _body(text, "void wave_sync"))
+    for kernel, steps in (("route_backward_kernel", (r"rows\[[^;]*\] = v\[", r"atomicAdd\(&rows\[", r"= rows\[")),
+                          ("balance_small_kernel", (r"count\[[^;]*\] = 0;", r"add_picks\([^;]*count"))):
+        body = _body(text, kernel)
+        at = [[m.start() for m in re.finditer(s, body)] for s in steps]
+        assert all(len(a) == 1 for a in at), (kernel, at)
+        for (a,), (b,) in zip(at, at[1:]):
+            assert a < b and len(re.findall(sync, body[a:b])) == 1, (kernel, a, b)
