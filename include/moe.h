@@ -360,7 +360,7 @@ MOE_API moe_status moe_fp8_linear(int32_t M, int32_t N, int32_t K, const void* c
  * w13 codes [E, 2I, H], scales [E, 2I / 128, H / 128]; w2 codes [E, H, I],
  * scales [E, H / 128, I / 128].  shape: dtype MOE_BF16 (the activations'),
  * activation MOE_SWIGLU, else MOE_ERR_UNSUPPORTED.  codes, x and y must be
- * aligned to 16 bytes, ws (moe_fp8_experts_workspace_bytes(shape) bytes, 0 for
+ * aligned to 16 bytes, scales, offsets and pairs to 4, ws (moe_fp8_experts_workspace_bytes(shape) bytes, 0 for
  * an unsupported shape) to 256.  T == 0 is a no-op. */
 MOE_API size_t moe_fp8_experts_workspace_bytes(const moe_shape* shape);
 MOE_API moe_status moe_fp8_experts(const moe_shape* shape, int32_t T, const void* w13_codes, const float* w13_scales,
@@ -400,7 +400,8 @@ MOE_API moe_status moe_balance_loss(int32_t T, int32_t E, int32_t k, const float
  *   - the losses of moe_balance_loss: d_loss fp32 [2] on the device, with
  *     counts and tokens as moe_balance_loss wrote them for the same batch
  *     (counts are constants of the gradient); NULL: none.
- * At least one of the two is given.  A masked token's row is zero, whatever
+ * At least one of the two is given.  Arrays of fp32 and int32 must be aligned to
+ * 4 bytes, here and in moe_balance_loss.  A masked token's row is zero, whatever
  * its inputs hold; that of a token in no sequence has the weights' part alone,
  * whatever its logits are.  d_logits must not overlap the inputs.  Limits as
  * above; no workspace. */

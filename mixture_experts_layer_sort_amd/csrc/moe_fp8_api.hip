@@ -28,6 +28,10 @@ int cu_count() {
 
 moe_status launched(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH; }
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+template <class... P>
+bool aligned4(const P*... p) {  // null is
+  return (aligned(p, 4) && ...);
+}
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // rows and columns of one weight matrix
@@ -161,6 +165,7 @@ moe_status moe_fp8_experts(const moe_shape* s, int32_t T, const void* w13_codes,
     return MOE_ERR_INVALID_ARG;
   if (!aligned(w13_codes, 16) || !aligned(w2_codes, 16) || !aligned(x, 16) || !aligned(y, 16) || !aligned(ws, 256))
     return MOE_ERR_INVALID_ARG;
+  if (!aligned4(w13_scales, w2_scales, offsets, sorted_pairs)) return MOE_ERR_INVALID_ARG;
   const ExpertsWorkspace W = experts_workspace(s);
   if (ws_bytes < W.total) return MOE_ERR_WORKSPACE;
   uint8_t* base = (uint8_t*)ws;
@@ -236,6 +241,7 @@ moe_status moe_balance_loss(int32_t T, int32_t E, int32_t k, const float* logits
   const moe_status st = check_router(T, E, k, token_mask, num_seqs, seq_offsets, balance_coef, z_coef);
   if (st != MOE_OK || T == 0) return st;
   if (!logits || !topk_ids || !loss || !counts || !tokens || !ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(logits, topk_ids, seq_offsets, loss, counts, tokens)) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < balance_workspace(T, E, num_seqs).total) return MOE_ERR_WORKSPACE;
   BalanceArgs a = {};
   a.logits = logits, a.ids = topk_ids, a.mask = token_mask, a.seq = seq_offsets;
@@ -254,6 +260,8 @@ moe_status moe_route_backward(int32_t T, int32_t E, int32_t k, const float* logi
   if (!logits || !d_logits || (!d_topk_w && !d_loss)) return MOE_ERR_INVALID_ARG;
   if (d_topk_w && (!topk_w || !topk_ids)) return MOE_ERR_INVALID_ARG;
   if (d_loss && (!counts || !tokens)) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(logits, topk_ids, topk_w, d_topk_w, seq_offsets, counts, tokens, d_loss, d_logits))
+    return MOE_ERR_INVALID_ARG;
   BalanceArgs a = {};
   a.logits = logits, a.ids = topk_ids, a.mask = token_mask, a.seq = seq_offsets;
   a.T = T, a.E = E, a.k = k, a.S = num_seqs;

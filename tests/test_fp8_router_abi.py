@@ -129,3 +129,17 @@ def test_workspace_of_a_large_batch_serves_smaller_ones():
     assert f(5000, 64, 1) <= f(5000, 64, 2) <= f(5000, 64, 1000) <= f(5000, 64, 65536)
     assert f(5000, 1, 3) <= f(5000, 64, 3) <= f(5000, 65, 3) <= f(5000, 1024, 3)
     assert balance(T=16384, E=256, S=16, seq=A, nbytes=f(16384, 256, 16) - 1) == WORKSPACE
+
+
+@pytest.mark.parametrize("name", ["s13", "s2", "off", "pairs"])
+def test_experts_refuse_odd_addresses(name):
+    assert experts(**{name: A + 2}) == INVALID and experts(**{name: A + 1}) == INVALID
+
+
+@pytest.mark.parametrize("call,names", [
+    (balance, ("logits", "ids", "seq", "loss", "counts", "tokens")),
+    (backward, ("logits", "ids", "w", "dw", "seq", "counts", "tokens", "dl", "out")),
+])
+def test_router_refuses_odd_addresses(call, names):
+    for name in names:
+        assert call(**{"seq": A, name: A + 2}) == INVALID, name
