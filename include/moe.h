@@ -330,7 +330,8 @@ MOE_API moe_status moe_nvfp4_linear(int32_t M, int32_t N, int32_t K, const void*
 
 /* Quantise `count` stacked fp32 matrices [rows, K] into that form (a block's
  * amax is over its 128 x 128 values).  K % 16 == 0, rows >= 1, both at most
- * 2^20 (else MOE_ERR_UNSUPPORTED); w aligned to 16 bytes, codes to 4. */
+ * 2^20, fewer than 2^24 blocks in all (else MOE_ERR_UNSUPPORTED); w aligned to
+ * 16 bytes, codes and scales to 4. */
 MOE_API moe_status moe_fp8_quantize_weights(int32_t count, int32_t rows, int32_t K, const float* w, void* codes,
                                             float* scales, hipStream_t stream);
 

@@ -99,7 +99,7 @@ moe_status moe_fp8_quantize_weights(int32_t count, int32_t rows, int32_t K, cons
   if (count < 0) return MOE_ERR_INVALID_ARG;
   if (!fp8_shape_ok(rows, K)) return MOE_ERR_UNSUPPORTED;
   const long long blocks = (long long)count * ((rows + 127) / 128) * ((K + 127) / 128);
-  if (blocks > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
+  if (blocks >= 1LL << 24) return MOE_ERR_UNSUPPORTED;  // a launch has fewer than 2^32 threads; 256 per block here
   if (count == 0) return MOE_OK;
   if (!w || !codes || !scales || !aligned(w, 16) || !aligned(codes, 4) || !aligned(scales, 4))
     return MOE_ERR_INVALID_ARG;

@@ -143,3 +143,10 @@ def test_experts_refuse_odd_addresses(name):
 def test_router_refuses_odd_addresses(call, names):
     for name in names:
         assert call(**{"seq": A, name: A + 2}) == INVALID, name
+
+
+def test_quantize_weights_refuses_more_blocks_than_a_launch_has():
+    """A launch has fewer than 2^32 threads, and a block of 128 x 128 weights takes 256."""
+    f = lib.load().moe_fp8_quantize_weights
+    assert f(1 << 24, 1, 16, A, A, A, None) == UNSUPPORTED and f(1 << 22, 129, 144, A, A, A, None) == UNSUPPORTED
+    assert f((1 << 24) - 1, 1, 16, None, A, A, None) == INVALID
