@@ -49,3 +49,55 @@ def test_rows_in_no_sequence_have_no_part(T):
         assert all(torch.equal(x, y) for x, y in zip(a, b)), bad
         assert np.array_equal(ga, tr._grad(logits, ids, off, None, 0.5, 0.25, w, dw, dl, a[1], a[2])), bad
         assert np.array_equal(la, tr._grad(logits, ids, off, None, 0.5, 0.25, None, None, dl, a[1], a[2])), bad
+
+
+@pytest.mark.parametrize("T,E,k,S", [(3000, 64, 6, 1000), (90, 256, 8, 5000), (300, 33, 2, 65536)])
+def test_many_sequences(T, E, k, S):
+    """Hundreds of sequences and more, most of them of a few tokens or none."""
+    rng, logits, ids, off, mask = tr._case(T, E, k, S, True, 23)
+    mask = (rng.random(T) < 0.8).astype(np.uint8)
+    loss, counts, tokens = tr._loss(logits, ids, off, mask, 0.01, 0.001)
+    rl, rc, rt = router.balance_loss(logits, ids, 0.01, 0.001, mask, off)
+    assert np.array_equal(counts.cpu().numpy(), rc) and np.array_equal(tokens.cpu().numpy(), rt)
+    assert np.all(np.abs(loss.double().cpu().numpy() - rl) <= tr.TOL * np.abs(rl))
+    again = tr._loss(logits, ids, off, mask, 0.01, 0.001)
+    assert torch.equal(again[0], loss)
+    w, dw = rng.random(ids.shape).astype(np.float32), rng.standard_normal(ids.shape).astype(np.float32)
+    ref, mag = router.backward(logits, ids, w, dw, (1.0, 1.0), 0.01, 0.001, mask, off)
+    g = tr._grad(logits, ids, off, mask, 0.01, 0.001, w, dw, np.ones(2, np.float32), counts, tokens)
+    assert np.all(np.abs(g - ref) <= tr.TOL * mag)
+
+
+def test_offsets_beyond_32_bits():
+    """Logits of over 2^31 values: the losses and counts of all of them, the gradient's first and last rows, and those
+    around 2^31 values, against torch in float64."""
+    d, (T, E, k) = gh.dev(), ((1 << 21) + 5, 1024, 2)
+    g = torch.Generator(device=d)
+    g.manual_seed(24)
+    logits = torch.empty(T, E, device=d)
+    logits.normal_(generator=g)
+    ids = torch.randint(0, E, (T, k), generator=g, device=d, dtype=torch.int32)
+    loss, counts = torch.empty(2, device=d), torch.empty(1, E, dtype=torch.int32, device=d)
+    tokens = torch.empty(1, dtype=torch.int32, device=d)
+    ws = torch.empty(lib.moe_balance_loss_workspace_bytes(T, E), dtype=torch.uint8, device=d)
+    lib.moe_balance_loss(T, E, k, logits, ids, loss, counts, tokens, ws, 0.01, 0.001)
+    P, z = torch.zeros(E, dtype=torch.float64, device=d), 0.0
+    for t in range(0, T, 1 << 17):
+        v = logits[t:t + (1 << 17)].double()
+        P += torch.softmax(v, 1).sum(0)
+        z += float(torch.logsumexp(v, 1).square().sum())
+    c = torch.bincount(ids.reshape(-1).long(), minlength=E)
+    assert torch.equal(counts[0].long(), c) and int(tokens) == T
+    ref = [0.01 * float((E * c.double() / (k * T) * P / T).sum()), 0.001 * z / T]
+    assert all(abs(a - b) <= tr.TOL * abs(b) for a, b in zip(loss.tolist(), ref))
+    out = torch.empty(T, E, device=d)
+    lib.moe_route_backward(T, E, k, logits, ids, out, d_loss=torch.ones(2, device=d), counts=counts, tokens=tokens,
+                           balance_coef=0.01, z_coef=0.001)
+    torch.cuda.synchronize()
+    f = 0.01 / T * (E * c.double() / (k * T) - 1.0)
+    for t in (0, (1 << 21) - 4, T - 8):
+        v = logits[t:t + 8].double()
+        p, zt = torch.softmax(v, 1), 2e-3 / T * torch.logsumexp(v, 1)[:, None]
+        want = p * (f - (p * f).sum(1, keepdim=True)) + zt * p
+        mag = p * (f.abs() + (p * f.abs()).sum(1, keepdim=True) + zt.abs())
+        assert bool(((out[t:t + 8].double() - want).abs() <= tr.TOL * mag).all()), t
