@@ -69,13 +69,14 @@ def act_bytes_per_elem(dtype):
 
 
 # sources of operators that the measured layer does not run and does not include
-OTHER_SOURCES = ("moe_fp8", "moe_balance")
+OTHER_SOURCES = ("moe_balance.h", "moe_balance.hip", "moe_fp8.h", "moe_fp8_api.hip", "moe_fp8_quant.hip",
+                 "moe_fp8_stream.hip", "moe_fp8_tile.hip")
 
 
 def kernel_source_hash():
     """Hash of every kernel source of the layer (the counters describe one build)."""
     h = hashlib.sha256()
-    for name in sorted(n for n in os.listdir(CSRC) if not n.startswith(OTHER_SOURCES)):
+    for name in sorted(n for n in os.listdir(CSRC) if n not in OTHER_SOURCES):
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode() + f.read())
     return h.hexdigest()[:16]

@@ -66,3 +66,19 @@ def test_lanes_that_share_lds_are_ordered():
         assert all(len(a) == 1 for a in at), (kernel, at)
         for (a,), (b,) in zip(at, at[1:]):
             assert a < b and len(re.findall(sync, body[a:b])) == 1, (kernel, a, b)
+
+
+def test_traffic_records_follow_every_source_of_the_layer(tmp_path, monkeypatch):
+    """The hash that the layer's traffic records carry leaves out other operators' files by their whole names: a new
+    source counts, whatever its name begins with."""
+    import bench
+
+    before = bench.kernel_source_hash()
+    for path in glob.glob(os.path.join(CSRC, "*")):
+        (tmp_path / os.path.basename(path)).write_bytes(open(path, "rb").read())
+    monkeypatch.setattr(bench, "CSRC", str(tmp_path))
+    assert bench.kernel_source_hash() == before
+    (tmp_path / "moe_fp8_tile.hip").write_text("// another")
+    assert bench.kernel_source_hash() == before
+    (tmp_path / "moe_fp8_layer.h").write_text("// new")
+    assert bench.kernel_source_hash() != before
