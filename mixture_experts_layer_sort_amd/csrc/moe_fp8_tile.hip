@@ -28,9 +28,11 @@
 //   start(kb): X(kb) has landed, everyone is done with stage kb - 1; Y(kb + 1) is issued
 //   mid(kb):   Y(kb) has landed, everyone is done with X(kb);        X(kb + 2) is issued
 //
-// Measured: 8192 x 4096 x 7168 in 208 us (2.3 PFLOP/s; 231 with the quantiser); 500 x 2816 x 4096 in 17 us; experts of
-// 8192 tokens (256 experts, top-8, H 7168, I 2048) 2.6 ms gate / up and 1.5 ms down (1.4 PFLOP/s: the tiles are two
-// thirds full); of 333 tokens (64 experts, top-6, H 4096, I 1408) 272 us, 4.1 TB/s of weights.
+// Measured (calls in runs of many, which hold the clock up; a launch by itself under a trace: median of 20):
+// 8192 x 4096 x 7168 in 226-239 us with the quantiser's 31 (2.1 PFLOP/s; product by itself 233, at best 200);
+// 500 x 2816 x 4096 in 19-20 us with the quantiser (product by itself 18.6); experts of 8192 tokens (256 experts, top-8,
+// H 7168, I 2048) 4.0-4.1 ms, 2.57 gate / up and 1.39 down (1.4 PFLOP/s: the tiles are two thirds full); of 333 tokens (64
+// experts, top-6, H 4096, I 1408) 255-268 us, 4.1-4.4 TB/s of weights.
 #include "moe_fp8.h"
 
 namespace moe {
