@@ -69,8 +69,10 @@ def act_bytes_per_elem(dtype):
 
 
 # sources of operators that the measured layer does not run and does not include
-OTHER_SOURCES = ("moe_balance.h", "moe_balance.hip", "moe_fp8.h", "moe_fp8_api.hip", "moe_fp8_quant.hip",
-                 "moe_fp8_stream.hip", "moe_fp8_tile.hip")
+OTHER_SOURCES = ("moe_balance.h", "moe_balance.hip", "moe_block_api.hip", "moe_fp8.h", "moe_fp8_api.hip",
+                 "moe_fp8_quant.hip", "moe_fp8_stream.hip", "moe_fp8_tile.hip", "moe_int8.h", "moe_int8_api.hip",
+                 "moe_int8_quant.hip", "moe_int8_stream.hip", "moe_int8_tile.hip", "moe_norm.h", "moe_norm.hip",
+                 "moe_router.h", "moe_router.hip", "moe_tiles.h", "moe_wave.h")
 
 
 def kernel_source_hash():

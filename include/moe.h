@@ -418,6 +418,149 @@ MOE_API moe_status moe_route_backward(int32_t T, int32_t E, int32_t k, const flo
                                       const int32_t* counts, const int32_t* tokens, const float* d_loss,
                                       float* d_logits, hipStream_t stream);
 
+/* ---- Routing by scores ------------------------------------------------------
+ * Top-k experts of every token by scores of all experts:
+ *   s = softmax(logits_t) or sigmoid(logits_t), c_e = fp32(fp32(s_e) + bias_e)
+ * (bias fp32 [E] has a part in the choice only; NULL: 0).  An expert whose logit
+ * is -inf is switched off: its c is -inf and its score 0.  Experts come in
+ * num_groups groups of consecutive ids; a group's score is its largest c
+ * (group_top = 1) or the fp32 sum of its two largest (2), and the topk_groups
+ * groups with the largest scores are kept (equal ones: the lower first).  Picks
+ * are the top_k largest c of the kept groups' experts in that order (equal ones:
+ * the lower id first; -0 == +0), each expert once; weights are
+ *   topk_w[t, j] = scale * s_j / (renormalise ? sum of the picks' s : 1)
+ * (0 where that sum is 0).  Scores are computed in 64 bits and weights rounded
+ * once, so the picks are those of the formulas above.  A row with a NaN (or, for
+ * softmax, +inf) gives NaN weights where they depend on it; ids are always in
+ * [0, E) and different from each other.
+ * Supported: 1 <= num_experts <= 1024, 1 <= top_k <= min(num_experts, 32),
+ * num_groups a divisor of num_experts, topk_groups groups hold top_k experts,
+ * group_top 1 or 2 and no larger than a group; T top_k <= 2^24, row strides at
+ * most 2^32 (else MOE_ERR_UNSUPPORTED). */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+  int32_t num_experts; /* E */
+  int32_t top_k;       /* k */
+  int32_t score;       /* moe_score */
+  int32_t num_groups;  /* 1: no groups */
+  int32_t topk_groups;
+  int32_t group_top;   /* choices of a group that count for it, 1 or 2 */
+  int32_t renormalise; /* 0 or 1 */
+  float scale;         /* finite */
+} moe_router;
+
+/* logits fp32 [T, E], rows logits_stride elements apart (>= E), any alignment of
+ * 4 bytes; topk_ids int32 [T, k], topk_w fp32 [T, k]: moe_permute's and
+ * moe_combine's inputs.  T == 0 is a no-op. */
+MOE_API moe_status moe_route_scores(const moe_router* router, int32_t T, const float* logits, int64_t logits_stride,
+                                    const float* bias, int32_t* topk_ids, float* topk_w, hipStream_t stream);
+
+/* Gradient of the logits through those weights: d_logits fp32 [T, E] (rows
+ * d_logits_stride apart) from d_topk_w fp32 [T, k] and the picks topk_ids (ids
+ * outside [0, E) have no part; an id that a row holds twice counts twice).  The
+ * choice itself has no gradient, so bias and groups do not appear.
+ * accumulate = 1 adds to d_logits instead of writing it (the losses' part comes
+ * from moe_route_backward with d_topk_w = NULL).  A token with token_mask[t] == 0
+ * (u8 [T]; NULL: all count) adds nothing: its row is zero, whatever its inputs
+ * hold, or left as it is.  d_logits must not overlap the inputs.  Limits as
+ * above. */
+MOE_API moe_status moe_route_scores_backward(const moe_router* router, int32_t T, const float* logits,
+                                             int64_t logits_stride, const int32_t* topk_ids, const float* d_topk_w,
+                                             const uint8_t* token_mask, int32_t accumulate, float* d_logits,
+                                             int64_t d_logits_stride, hipStream_t stream);
+
+/* ---- Products on 8-bit integer weights --------------------------------------
+ * Weights as int8 codes [N, K] with one fp32 scale per output channel, [N]
+ * (weight = code * scale).  Activations are bf16 rows, quantised inside with one
+ * scale per row: amax = max(max |x|, 2^-100), scale = fp32(amax / 127), code =
+ * round(fp32(x * fp32(127 / amax))), ties to even.  Sums of products of codes are
+ * exact 32-bit integers, and an output is bf16(fp32(fp32(sum) * scale of the row) *
+ * scale of the channel)): a token's bits do not depend on the batch around it.
+ * A row that holds an infinity or a NaN gives NaN in every column. */
+
+/* Quantise `count` stacked fp32 matrices [rows, K] into that form (a channel's
+ * amax is over its K values; a channel with an infinity or a NaN gets the scale
+ * NaN).  K % 16 == 0, K <= 2^17, 1 <= rows <= 2^20, fewer than 2^24 rows in all
+ * (else MOE_ERR_UNSUPPORTED); w aligned to 16 bytes, codes and scales to 4. */
+MOE_API moe_status moe_int8_quantize_weights(int32_t count, int32_t rows, int32_t K, const float* w, void* codes,
+                                             float* scales, hipStream_t stream);
+
+/* Dense linear layer: out[m, n] = bf16( scale_m scale_n sum_k code(x)[m, k] code[n, k] ).
+ * x bf16 [M, K] with rows x_stride elements apart (>= K, a multiple of 8), out
+ * bf16 [M, N] with rows out_stride elements apart (>= N); columns past N of an
+ * out row are left as they are.  Any 1 <= N <= 2^20; K a multiple of 16, at most
+ * 2^17; both strides at most 2^32 (else MOE_ERR_UNSUPPORTED); M <= 2^24, 0 is a
+ * no-op.  codes and x must be aligned to 16 bytes, scales to 4, ws to 256.
+ * Workspace: moe_int8_linear_workspace_bytes(max_M, N, K) bytes serve any M <=
+ * max_M (0 for unsupported arguments); its contents need not survive a call. */
+MOE_API size_t moe_int8_linear_workspace_bytes(int32_t max_M, int32_t N, int32_t K);
+MOE_API moe_status moe_int8_linear(int32_t M, int32_t N, int32_t K, const void* codes, const float* scales,
+                                   const uint16_t* x, int64_t x_stride, uint16_t* out, int64_t out_stride, void* ws,
+                                   size_t ws_bytes, hipStream_t stream);
+
+/* The expert MLPs of routed tokens on such weights: for sorted row r of expert
+ * e, p = sorted_pairs[r], t = p / top_k:
+ *   g, u = W13[e] . quant(x[t]) (rows [0, I) gate, [I, 2I) up; the shape's
+ *   gate_up_limit as in moe_gemm13_swiglu_quant, a NaN stays one),
+ *   h = bf16(silu(g) * u),
+ *   y[p] = bf16( W2[e] . quant(h) ).
+ * offsets [E + 1] and sorted_pairs [T top_k] are moe_permute's outputs, x is
+ * bf16 [T, H], y bf16 [T top_k, H] (the input of moe_combine and
+ * moe_combine_norm).  w13 codes [E, 2I, H], scales [E, 2I]; w2 codes [E, H, I],
+ * scales [E, H].  shape: dtype MOE_BF16 (the activations'), activation
+ * MOE_SWIGLU, hidden and inter at most 2^17, else MOE_ERR_UNSUPPORTED.  codes, x
+ * and y must be aligned to 16 bytes, scales, offsets and pairs to 4, ws
+ * (moe_int8_experts_workspace_bytes(shape) bytes, 0 for an unsupported shape) to
+ * 256.  T == 0 is a no-op. */
+MOE_API size_t moe_int8_experts_workspace_bytes(const moe_shape* shape);
+MOE_API moe_status moe_int8_experts(const moe_shape* shape, int32_t T, const void* w13_codes, const float* w13_scales,
+                                    const void* w2_codes, const float* w2_scales, const int32_t* offsets,
+                                    const int32_t* sorted_pairs, const uint16_t* x, uint16_t* y, void* ws,
+                                    size_t ws_bytes, hipStream_t stream);
+
+/* ---- The end of an expert block ---------------------------------------------
+ * moe_combine joined with what follows it in a layer, for every token, in fp32:
+ *   m = sum_j topk_w[t, j] y[t k + j] + shared_gate[t] shared[t]
+ *   n = m / sqrt(mean(m^2) + eps) * post_weight   (NULL: n = m)
+ *   r = residual[t] + scale * n                   out[t] = bf16(r)
+ *   normed[t] = bf16( r / sqrt(mean(r^2) + eps) * next_weight )
+ * y bf16 [T k, H] and topk_w fp32 [T, k] (NULL, both, with k = 0: no routed
+ * experts), shared bf16 [T, H] (NULL: none; needed with k = 0) with shared_gate
+ * fp32 [T] (NULL: 1), residual bf16 [T, H] (NULL: 0), post_weight and next_weight
+ * bf16 [H]; normed is given with next_weight or not at all.  With k = 0 it is the
+ * norm around any other block: shared is that block's output, or the stream
+ * itself with no residual.  out may be the residual; else outputs must not overlap
+ * inputs.  8 <= H <= 16384, H % 8 == 0, 0 <= k <= 32, T and T k at most 2^24 (else
+ * MOE_ERR_UNSUPPORTED); eps >= 0 and scale finite.  bf16 arrays must be aligned
+ * to 16 bytes, fp32 ones to 4. */
+MOE_API moe_status moe_combine_norm(int32_t T, int32_t H, int32_t k, const uint16_t* y, const float* topk_w,
+                                    const uint16_t* shared, const float* shared_gate, const uint16_t* residual,
+                                    const uint16_t* post_weight, const uint16_t* next_weight, float eps, float scale,
+                                    uint16_t* out, uint16_t* normed, hipStream_t stream);
+
+/* Its gradients, from d_out bf16 [T, H] (NULL: 0) and d_normed bf16 [T, H] (with
+ * next_weight), the forward pass's inputs and its out (needed with next_weight;
+ * the next norm's gradient is taken at the stored rows):
+ *   d_residual bf16 [T, H], d_y bf16 [T k, H], d_topk_w fp32 [T, k] (what
+ *   moe_route_scores_backward and moe_route_backward take), d_shared bf16 [T, H],
+ *   d_gate fp32 [T]: each NULL if it is not wanted;
+ *   d_post_weight, d_next_weight fp32 [H]: given with their weights; sums over the
+ *   tokens in an order that depends on T alone.
+ * d_residual may be d_out; else outputs must not overlap inputs.  Workspace (with
+ * post_weight or next_weight): moe_combine_norm_backward_workspace_bytes(max_T, H)
+ * bytes serve any T <= max_T (0 for unsupported arguments), aligned to 256; need
+ * not be cleared, and calls that share it must be stream-ordered.  T == 0 is a
+ * no-op (the weights' gradients are then not written).  Limits as above. */
+MOE_API size_t moe_combine_norm_backward_workspace_bytes(int32_t max_T, int32_t H);
+MOE_API moe_status moe_combine_norm_backward(int32_t T, int32_t H, int32_t k, const uint16_t* y, const float* topk_w,
+                                             const uint16_t* shared, const float* shared_gate, const uint16_t* out,
+                                             const uint16_t* post_weight, const uint16_t* next_weight, float eps,
+                                             float scale, const uint16_t* d_out, const uint16_t* d_normed,
+                                             uint16_t* d_residual, uint16_t* d_y, float* d_topk_w, uint16_t* d_shared,
+                                             float* d_gate, float* d_post_weight, float* d_next_weight, void* ws,
+                                             size_t ws_bytes, hipStream_t stream);
+
 /* Size of the device scratch array behind moe_forward_noalloc (64 MiB per
  * device, held until the process ends). */
 #define MOE_NOALLOC_SCRATCH_BYTES (64u << 20)

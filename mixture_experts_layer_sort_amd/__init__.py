@@ -22,6 +22,9 @@ DTYPES = {"bf16": MOE_BF16, "mxfp8": MOE_MXFP8, "nvfp4": MOE_NVFP4, "bf16_mxfp8"
 # expert activations: gated SwiGLU (W13 of 2I rows) or non-gated squared ReLU (W1 of I rows)
 MOE_SWIGLU, MOE_RELU2 = 0, 1
 ACTIVATIONS = {"swiglu": MOE_SWIGLU, "relu2": MOE_RELU2}
+# scores of the routing by scores
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 
 EXPORTED = [
     "moe_status_string",
@@ -63,6 +66,16 @@ EXPORTED = [
     "moe_balance_loss_workspace_bytes",
     "moe_balance_loss",
     "moe_route_backward",
+    "moe_route_scores",
+    "moe_route_scores_backward",
+    "moe_int8_quantize_weights",
+    "moe_int8_linear_workspace_bytes",
+    "moe_int8_linear",
+    "moe_int8_experts_workspace_bytes",
+    "moe_int8_experts",
+    "moe_combine_norm",
+    "moe_combine_norm_backward_workspace_bytes",
+    "moe_combine_norm_backward",
 ]
 
 
@@ -86,6 +99,23 @@ class moe_shape(ctypes.Structure):
         return (f"moe_shape(H={self.hidden}, I={self.inter}, E={self.num_experts}, k={self.top_k}, "
                 f"max_tokens={self.max_tokens}, dtype={self.dtype}, activation={self.activation}, "
                 f"gate_up_limit={self.gate_up_limit})")
+
+
+class moe_router(ctypes.Structure):
+    _fields_ = [
+        ("num_experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("renormalise", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+    def __repr__(self):
+        return (f"moe_router(E={self.num_experts}, k={self.top_k}, score={self.score}, groups={self.topk_groups} of "
+                f"{self.num_groups}, group_top={self.group_top}, renormalise={self.renormalise}, scale={self.scale})")
 
 
 class moe_knobs(ctypes.Structure):
@@ -122,11 +152,18 @@ def make_shape(hidden, inter, num_experts, top_k, max_tokens, dtype, activation=
     return moe_shape(hidden, inter, num_experts, top_k, max_tokens, d, a, gate_up_limit)
 
 
+def make_router(num_experts, top_k, score="softmax", num_groups=1, topk_groups=1, group_top=1, renormalise=True,
+                scale=1.0) -> moe_router:
+    c = SCORES[score] if isinstance(score, str) else int(score)
+    return moe_router(num_experts, top_k, c, num_groups, topk_groups, group_top, int(renormalise), scale)
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m mixture_experts_layer_sort_amd.build`")
     lib = ctypes.CDLL(LIB_PATH)
     P, S, I32, SZ = ctypes.c_void_p, ctypes.POINTER(moe_shape), ctypes.c_int32, ctypes.c_size_t
+    R = ctypes.POINTER(moe_router)
     I64, F32 = ctypes.c_int64, ctypes.c_float
     sig = {
         "moe_status_string": (ctypes.c_char_p, [I32]),
@@ -169,6 +206,17 @@ def _load():
         "moe_balance_loss_workspace_bytes": (SZ, [I32, I32, I32]),
         "moe_balance_loss": (I32, [I32, I32, I32, P, P, P, I32, P, F32, F32, P, P, P, P, SZ, P]),
         "moe_route_backward": (I32, [I32, I32, I32, P, P, P, P, P, I32, P, F32, F32, P, P, P, P, P]),
+        "moe_route_scores": (I32, [R, I32, P, I64, P, P, P, P]),
+        "moe_route_scores_backward": (I32, [R, I32, P, I64, P, P, P, I32, P, I64, P]),
+        "moe_int8_quantize_weights": (I32, [I32, I32, I32, P, P, P, P]),
+        "moe_int8_linear_workspace_bytes": (SZ, [I32, I32, I32]),
+        "moe_int8_linear": (I32, [I32, I32, I32, P, P, P, I64, P, I64, P, SZ, P]),
+        "moe_int8_experts_workspace_bytes": (SZ, [S]),
+        "moe_int8_experts": (I32, [S, I32, P, P, P, P, P, P, P, P, P, SZ, P]),
+        "moe_combine_norm": (I32, [I32, I32, I32, P, P, P, P, P, P, P, F32, F32, P, P, P]),
+        "moe_combine_norm_backward_workspace_bytes": (SZ, [I32, I32]),
+        "moe_combine_norm_backward": (I32, [I32, I32, I32, P, P, P, P, P, P, P, F32, F32, P, P, P, P, P, P, P, P, P,
+                                            P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -466,3 +514,77 @@ def moe_route_backward(T, E, k, logits, topk_ids, d_logits, topk_w=None, d_topk_
     _check(_lib.moe_route_backward(T, E, k, _ptr(logits), _ptr(topk_ids), _ptr(topk_w), _ptr(d_topk_w),
                                    _ptr(token_mask), num_seqs, _ptr(seq_offsets), balance_coef, z_coef, _ptr(counts),
                                    _ptr(tokens), _ptr(d_loss), _ptr(d_logits), _stream(stream)), "moe_route_backward")
+
+
+def moe_route_scores(router, T, logits, topk_ids, topk_w, bias=None, logits_stride=None, stream=None):
+    """topk_ids int32 [T, k], topk_w fp32 [T, k] of logits fp32 [T, E] (row stride in elements, default E)."""
+    _check(_lib.moe_route_scores(ctypes.byref(router), T, _ptr(logits),
+                                 router.num_experts if logits_stride is None else logits_stride, _ptr(bias),
+                                 _ptr(topk_ids), _ptr(topk_w), _stream(stream)), "moe_route_scores")
+
+
+def moe_route_scores_backward(router, T, logits, topk_ids, d_topk_w, d_logits, token_mask=None, accumulate=False,
+                              logits_stride=None, d_logits_stride=None, stream=None):
+    """d_logits fp32 [T, E] from d_topk_w fp32 [T, k]; accumulate: added to what is there."""
+    E = router.num_experts
+    _check(_lib.moe_route_scores_backward(ctypes.byref(router), T, _ptr(logits),
+                                          E if logits_stride is None else logits_stride, _ptr(topk_ids),
+                                          _ptr(d_topk_w), _ptr(token_mask), int(accumulate), _ptr(d_logits),
+                                          E if d_logits_stride is None else d_logits_stride, _stream(stream)),
+           "moe_route_scores_backward")
+
+
+def moe_int8_quantize_weights(count, rows, K, w, codes, scales, stream=None):
+    """int8 codes [count, rows, K] and fp32 scales [count, rows] of fp32 matrices w [count, rows, K]."""
+    _check(_lib.moe_int8_quantize_weights(count, rows, K, _ptr(w), _ptr(codes), _ptr(scales), _stream(stream)),
+           "moe_int8_quantize_weights")
+
+
+def moe_int8_linear_workspace_bytes(max_M: int, N: int, K: int) -> int:
+    return _lib.moe_int8_linear_workspace_bytes(max_M, N, K)
+
+
+def moe_int8_linear(M, N, K, codes, scales, x, out, ws, x_stride=None, out_stride=None, ws_bytes=None, stream=None):
+    """out bf16 [M, N] = quant(x bf16 [M, K]) . W^T on int8 weights; row strides in elements (default K, N)."""
+    nbytes = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check(_lib.moe_int8_linear(M, N, K, _ptr(codes), _ptr(scales), _ptr(x), K if x_stride is None else x_stride,
+                                _ptr(out), N if out_stride is None else out_stride, _ptr(ws), nbytes,
+                                _stream(stream)), "moe_int8_linear")
+
+
+def moe_int8_experts_workspace_bytes(shape: moe_shape) -> int:
+    return _lib.moe_int8_experts_workspace_bytes(ctypes.byref(shape))
+
+
+def moe_int8_experts(shape, T, w13_codes, w13_scales, w2_codes, w2_scales, offsets, sorted_pairs, x, y, ws,
+                     ws_bytes=None, stream=None):
+    """Expert MLPs of routed tokens on int8 weights: y bf16 [T * top_k, H], rows by pair."""
+    nbytes = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check(_lib.moe_int8_experts(ctypes.byref(shape), T, _ptr(w13_codes), _ptr(w13_scales), _ptr(w2_codes),
+                                 _ptr(w2_scales), _ptr(offsets), _ptr(sorted_pairs), _ptr(x), _ptr(y), _ptr(ws),
+                                 nbytes, _stream(stream)), "moe_int8_experts")
+
+
+def moe_combine_norm(T, H, k, out, normed=None, y=None, topk_w=None, shared=None, shared_gate=None, residual=None,
+                     post_weight=None, next_weight=None, scale=1.0, eps=1e-6, stream=None):
+    """out bf16 [T, H] = residual + scale * norm(sum_j w_j y_j + gate shared), normed = norm(out) (see include/moe.h)."""
+    _check(_lib.moe_combine_norm(T, H, k, _ptr(y), _ptr(topk_w), _ptr(shared), _ptr(shared_gate), _ptr(residual),
+                                 _ptr(post_weight), _ptr(next_weight), eps, scale, _ptr(out), _ptr(normed),
+                                 _stream(stream)), "moe_combine_norm")
+
+
+def moe_combine_norm_backward_workspace_bytes(max_T: int, H: int) -> int:
+    return _lib.moe_combine_norm_backward_workspace_bytes(max_T, H)
+
+
+def moe_combine_norm_backward(T, H, k, d_out, d_normed=None, out=None, ws=None, y=None, topk_w=None, shared=None,
+                              shared_gate=None, post_weight=None, next_weight=None, scale=1.0, eps=1e-6,
+                              d_residual=None, d_y=None, d_topk_w=None, d_shared=None, d_gate=None,
+                              d_post_weight=None, d_next_weight=None, ws_bytes=None, stream=None):
+    """Gradients of moe_combine_norm's inputs; those not wanted None (the norm weights' come with their weights)."""
+    nbytes = ws_bytes if ws_bytes is not None else 0 if ws is None else ws.numel() * ws.element_size()
+    _check(_lib.moe_combine_norm_backward(T, H, k, _ptr(y), _ptr(topk_w), _ptr(shared), _ptr(shared_gate), _ptr(out),
+                                          _ptr(post_weight), _ptr(next_weight), eps, scale, _ptr(d_out),
+                                          _ptr(d_normed), _ptr(d_residual), _ptr(d_y), _ptr(d_topk_w),
+                                          _ptr(d_shared), _ptr(d_gate), _ptr(d_post_weight), _ptr(d_next_weight),
+                                          _ptr(ws), nbytes, _stream(stream)), "moe_combine_norm_backward")

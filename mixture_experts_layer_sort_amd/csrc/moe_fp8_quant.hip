@@ -1,5 +1,6 @@
 // Quantisers of the block-128 fp8 products.
 #include "moe_fp8.h"
+#include "moe_tiles.h"
 
 namespace moe {
 namespace {
@@ -44,47 +45,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_weights_kernel(int rows, int
 // (scales are stored column-block-major, so a tile's tokens read them in one
 // piece).  Bound by memory: 2 bytes in, 1 out per value.  The last block of a
 // grouped launch writes the token tiles instead.
-struct TileList {
-  const int* offsets;
-  int E, tile;
-  int4* tiles;
-  int* ntiles;
-};
-
 constexpr int kQCols = 512;
-
-__device__ __forceinline__ void write_tiles(const TileList& l) {
-  __shared__ int part[4];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  int base = 0;
-  for (int e0 = 0; e0 < l.E; e0 += 256) {
-    const int e = e0 + tid;
-    int first = 0, c = 0;
-    if (e < l.E) {
-      first = l.offsets[e];
-      c = (max(0, l.offsets[e + 1] - first) + l.tile - 1) / l.tile;
-    }
-    int s = c;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(s, d, 64);
-      if (lane >= d) s += o;
-    }
-    if (lane == 63) part[wv] = s;
-    __syncthreads();
-    int at = base + s - c;
-    for (int i = 0; i < 4; ++i) {
-      if (i < wv) at += part[i];
-      base += part[i];
-    }
-    for (int i = 0; i < c; ++i) {
-      const int g = i / kFp8TileGroup * kFp8TileGroup;
-      l.tiles[at + i] = make_int4(e, first + i * l.tile, at + g, min(kFp8TileGroup, c - g));
-    }
-    __syncthreads();
-  }
-  if (tid == 0) *l.ntiles = base;
-}
 
 template <int kQRows>
 __global__ __launch_bounds__(256) void fp8_quantize_rows_kernel(int M, int K, const uint16_t* x, long long ldx,
@@ -92,7 +53,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_rows_kernel(int M, int K, co
   __shared__ float sc[4][kQRows];
   const int KB = (K + kFp8Blk - 1) / kFp8Blk, Kp = KB * kFp8Blk, CB = (Kp + kQCols - 1) / kQCols;
   if (list.tiles && blockIdx.x == gridDim.x - 1) {
-    write_tiles(list);
+    write_tiles<kFp8TileGroup>(list);
     return;
   }
   const int cb = blockIdx.x % CB, m0 = blockIdx.x / CB * kQRows;

@@ -1,0 +1,354 @@
+// Streaming product on 8-bit integer weights: few token rows per weight matrix
+// (decoding), so the time is that of reading the weights once.
+//
+// Item = (token tile, R fragments of 16 weight rows).  The block's KS waves take
+// the 128-wide K steps in turn; a wave reads its weight fragment straight from the
+// row-major codes into the operand registers (lane r + 16 q: row r, bytes [16 q,
+// 16 q + 16) and [64 + 16 q, + 16) of the step; which 32 of the 128 bytes a lane
+// holds does not matter, since tokens use the same order), D steps ahead.  The
+// waves' integer sums meet in LDS.
+#include "moe_int8.h"
+
+namespace moe {
+namespace {
+
+// fp32 value of a sum: the same two products in every kernel.
+__device__ __forceinline__ float value(int acc, float sx, float sw) { return (float)acc * sx * sw; }
+
+// Columns n .. n + 3 of an output row that ends at N.
+__device__ __forceinline__ void store4(uint16_t* row, int n, int N, const f32x4& v) {
+  uint16_t* o = row + n;
+  const uint32_t b0 = f32_to_bf16(v[0]), b1 = f32_to_bf16(v[1]), b2 = f32_to_bf16(v[2]), b3 = f32_to_bf16(v[3]);
+  if (n + 4 <= N && ((uintptr_t)o & 7) == 0) {
+    *reinterpret_cast<uint2*>(o) = make_uint2(b0 | b1 << 16, b2 | b3 << 16);
+  } else {
+    if (n < N) o[0] = (uint16_t)b0;
+    if (n + 1 < N) o[1] = (uint16_t)b1;
+    if (n + 2 < N) o[2] = (uint16_t)b2;
+    if (n + 3 < N) o[3] = (uint16_t)b3;
+  }
+}
+
+// Dynamic LDS of the kernels that quantise into it, at most: the limit asked for on every call (the same number, whatever
+// other threads launch meanwhile).
+constexpr int kBlockLds = 64 * 1024;
+__host__ __device__ inline size_t block_lds(int rows, int K) { return (size_t)rows * (int8_pad(K) + 16); }
+
+// Rows `row(i)`, i < rows <= 16, of K bf16 values into LDS: codes [rows][Kp + 16] (the 16 rows of a fragment read start 4
+// banks apart), scales [rows].  Pieces of 8 values, 16 consecutive lanes in one row; the first HELD of a thread stay in
+// registers between the maximum and the codes, the others are read again.
+template <int HELD, class F>
+__device__ __forceinline__ void quantize_block(uint8_t* codes, float* scales, uint32_t* amax, int rows, int K, int tid,
+                                               int threads, F&& row) {
+  const int Kp = int8_pad(K), per = Kp / 8, n = rows * per;
+  const u32x4 none = {0, 0, 0, 0};
+  if (tid < 16) amax[tid] = __float_as_uint(kFp8Tiny);
+  u32x4 v[HELD];
+#pragma unroll
+  for (int u = 0; u < HELD; ++u) {
+    const int c = tid + u * threads, i = c / per, col = 8 * (c - i * per);
+    v[u] = c < n && col < K ? *reinterpret_cast<const u32x4*>(row(i) + col) : none;
+  }
+  __syncthreads();
+  auto top = [&](int c, const u32x4& x) {
+    const uint32_t m = fp8_amax8(x, kFp8TinyBits);
+    // magnitudes on their bits, so that a NaN, above everything, stays
+    uint32_t b = max(m << 16, m & 0xFFFF0000u);
+    b = max(b, __builtin_amdgcn_update_dpp(0u, b, 0x128, 0xF, 0xF, true));
+    b = max(b, __builtin_amdgcn_update_dpp(0u, b, 0x124, 0xF, 0xF, true));
+    b = max(b, __builtin_amdgcn_update_dpp(0u, b, 0x122, 0xF, 0xF, true));
+    b = max(b, __builtin_amdgcn_update_dpp(0u, b, 0x121, 0xF, 0xF, true));
+    if ((tid & 15) == 0) atomicMax(&amax[c / per], b);
+  };
+#pragma unroll
+  for (int u = 0; u < HELD; ++u)
+    if (tid + u * threads < n) top(tid + u * threads, v[u]);
+  for (int c = tid + HELD * threads; c < n; c += threads) {
+    const int i = c / per, col = 8 * (c - i * per);
+    top(c, col < K ? *reinterpret_cast<const u32x4*>(row(i) + col) : none);
+  }
+  __syncthreads();
+  auto put = [&](int c, const u32x4& x) {
+    const int i = c / per, col = 8 * (c - i * per);
+    float f, s;
+    int8_factor(__uint_as_float(amax[i]), f, s);
+    *reinterpret_cast<uint2*>(codes + i * (Kp + 16) + col) = int8_codes8(x, f);
+    if (col == 0) scales[i] = s;
+  };
+#pragma unroll
+  for (int u = 0; u < HELD; ++u)
+    if (tid + u * threads < n) put(tid + u * threads, v[u]);
+  for (int c = tid + HELD * threads; c < n; c += threads) {
+    const int i = c / per, col = 8 * (c - i * per);
+    put(c, col < K ? *reinterpret_cast<const u32x4*>(row(i) + col) : none);
+  }
+  __syncthreads();
+}
+
+template <int NT, int R, int KS, int D, Int8Mode MODE, bool BLOCK>
+__global__ __launch_bounds__(64 * KS) void int8_stream_kernel(Int8Args a) {
+  static_assert(!BLOCK || NT == 1, "one token fragment");
+  extern __shared__ __align__(16) uint8_t quantized[];  // BLOCK
+  __shared__ float qscale[16];
+  __shared__ uint32_t qmax[16];
+  __shared__ i32x4 red[KS][R * NT][64];
+  __shared__ int cum[MODE == INT8_DENSE ? 1 : 1025];
+  const int kRows = BLOCK ? a.cap : 16 * NT;
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int Kp = int8_pad(a.K), KB = Kp / 128;
+  // weight rows of one item: DENSE / DOWN 16 R consecutive ones; GATE_UP 8 R gate rows and the 8 R up rows
+  constexpr int kItemN = MODE == INT8_GATE_UP ? 8 * R : 16 * R;
+  const int nspan = MODE == INT8_GATE_UP ? a.N / 2 : a.N;
+  const int nitems = (nspan + kItemN - 1) / kItemN;
+
+  int total;  // token tiles
+  if constexpr (MODE == INT8_DENSE) {
+    total = (a.rows + kRows - 1) / kRows;
+  } else {
+    // prefix of the experts' token tiles: a scan over chunks of the block's size
+    int base = 0;
+    if (tid == 0) cum[0] = 0;
+    int* part = reinterpret_cast<int*>(&red[0][0][0]);
+    for (int e0 = 0; e0 < a.E; e0 += 64 * KS) {
+      const int e = e0 + tid;
+      int c = 0;
+      if (e < a.E) c = (max(0, a.offsets[e + 1] - a.offsets[e]) + kRows - 1) / kRows;
+      int s = c;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(s, d, 64);
+        if (lane >= d) s += o;
+      }
+      if (lane == 63) part[wv] = s;
+      __syncthreads();
+      int before = base, all = 0;
+      for (int i = 0; i < KS; ++i) {
+        if (i < wv) before += part[i];
+        all += part[i];
+      }
+      if (e < a.E) cum[e + 1] = before + s;
+      base += all;
+      __syncthreads();
+    }
+    total = base;
+  }
+
+  const long long items = (long long)total * nitems;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    // tiles of one weight slab run next to each other on one XCD (blocks go round the 8 XCDs)
+    int tile, slab;
+    {
+      const long long per = 8LL * total;
+      const long long g = it / per;
+      const int left = min(8LL, nitems - 8 * g);  // slabs of this group
+      const long long o = it - g * per;
+      slab = (int)(8 * g + o % left);
+      tile = (int)(o / left);
+    }
+    int e = 0, r0, rend;
+    if constexpr (MODE == INT8_DENSE) {
+      r0 = tile * kRows;
+      rend = min(a.rows, r0 + kRows);
+    } else {
+      int lo = 0, hi = a.E - 1;  // the expert with cum[e] <= tile < cum[e + 1]
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid + 1] > tile) hi = mid;
+        else lo = mid + 1;
+      }
+      e = lo;
+      r0 = max(0, a.offsets[e]) + (tile - cum[e]) * kRows;
+      rend = min(min(a.offsets[e + 1], a.rows), r0 + kRows);
+    }
+    auto source = [&](int row) { return MODE == INT8_GATE_UP ? a.pairs[row] / a.k : row; };
+    // weight fragments of this lane; rows past the end repeat the last one (results dropped)
+    auto first_row = [&](int f) {
+      return MODE == INT8_GATE_UP ? (f < R / 2 ? 0 : nspan) + slab * kItemN + 16 * (f % (R / 2)) : slab * kItemN + 16 * f;
+    };
+    const int8_t* wrow[R];
+#pragma unroll
+    for (int f = 0; f < R; ++f) wrow[f] = a.w + ((size_t)e * a.N + min(first_row(f) + r, a.N - 1)) * a.K + 16 * q;
+    const int8_t* qrow[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if constexpr (BLOCK) qrow[t] = reinterpret_cast<const int8_t*>(quantized) + min(r, rend - r0 - 1) * (Kp + 16) + 16 * q;
+      else qrow[t] = a.xq + (size_t)source(min(r0 + 16 * t + r, rend - 1)) * Kp + 16 * q;
+    }
+    i32x4 acc[R][NT];
+#pragma unroll
+    for (int f = 0; f < R; ++f)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[f][t] = i32x4{0, 0, 0, 0};
+
+    struct Step {
+      u32x4 w[R][2];
+      u32x4 x[BLOCK ? 1 : NT][2];
+    };
+    // Loads without branches around them (each would end in a wait for everything in flight): steps past the last one
+    // repeat it, and pieces past the end of a ragged K are the step's first (their tokens' codes are zero).
+    auto load = [&](Step& st, int step) {
+      const int kb = min(step, KB - 1);
+      const int lo = kb * 128 + 16 * q < a.K ? 0 : -16 * q, hi = kb * 128 + 64 + 16 * q < a.K ? 64 : -16 * q;
+#pragma unroll
+      for (int f = 0; f < R; ++f) {
+        const int8_t* p = wrow[f] + (size_t)kb * 128;
+        st.w[f][0] = *reinterpret_cast<const u32x4*>(p + lo);
+        st.w[f][1] = *reinterpret_cast<const u32x4*>(p + hi);
+      }
+      if constexpr (!BLOCK) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const u32x4* p = reinterpret_cast<const u32x4*>(qrow[t] + (size_t)kb * 128);
+          st.x[t][0] = p[0];
+          st.x[t][1] = p[4];
+        }
+      }
+    };
+    auto compute = [&](const Step& st, int kb) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        u32x4 lo, hi;
+        if constexpr (BLOCK) {
+          lo = *reinterpret_cast<const u32x4*>(qrow[t] + kb * 128);
+          hi = *reinterpret_cast<const u32x4*>(qrow[t] + kb * 128 + 64);
+        } else {
+          lo = st.x[t][0], hi = st.x[t][1];
+        }
+#pragma unroll
+        for (int f = 0; f < R; ++f) {
+          acc[f][t] = int8_mfma(st.w[f][0], lo, acc[f][t]);
+          acc[f][t] = int8_mfma(st.w[f][1], hi, acc[f][t]);
+        }
+      }
+    };
+    // this wave's steps wv, wv + KS, ...: D of them in flight
+    const int n = wv < KB ? (KB - wv + KS - 1) / KS : 0;
+    Step st[D];
+    if (n > 0) {
+#pragma unroll
+      for (int u = 0; u < D; ++u)
+        if (u == 0 || u < n) load(st[u], wv + u * KS);
+    }
+    if constexpr (BLOCK)  // while the first weights are on their way
+      quantize_block<4>(quantized, qscale, qmax, rend - r0, a.K, tid, 64 * KS,
+                        [&](int i) { return a.x + (size_t)source(r0 + i) * a.ldx; });
+    if (n > 0) {
+      int i = 0;
+      for (; i + 2 * D <= n; i += D) {
+#pragma unroll
+        for (int u = 0; u < D; ++u) {
+          compute(st[u], wv + (i + u) * KS);
+          load(st[u], wv + (i + u + D) * KS);
+        }
+      }
+      // fewer than 2 D steps are left, the first D of them loaded
+#pragma unroll
+      for (int u = 0; u < D; ++u)
+        if (i + u < n) {
+          compute(st[u], wv + (i + u) * KS);
+          if (i + u + D < n) load(st[u], wv + (i + u + D) * KS);
+        }
+#pragma unroll
+      for (int u = 0; u < D - 1; ++u)
+        if (i + u + D < n) compute(st[u], wv + (i + u + D) * KS);
+    }
+    // accumulator (f, t) element i of lane r + 16 q is weight row 16 f + 4 q + i, token 16 t + r
+#pragma unroll
+    for (int f = 0; f < R; ++f)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) red[wv][f * NT + t][lane] = acc[f][t];
+    __syncthreads();
+    constexpr int kUnits = MODE == INT8_GATE_UP ? R / 2 * NT : R * NT;
+    for (int u = wv; u < kUnits; u += KS) {
+      auto sum = [&](int j) {
+        i32x4 v = red[0][j][lane];
+#pragma unroll
+        for (int i = 1; i < KS; ++i) v += red[i][j][lane];
+        return v;
+      };
+      const int f = u / NT, t = u % NT, row = r0 + 16 * t + r;
+      if (row < rend) {
+        float sx;
+        if constexpr (BLOCK) sx = qscale[r];
+        else sx = a.xs[source(row)];
+        auto values = [&](int j, int n0) {
+          const i32x4 c = sum(j);
+          f32x4 v;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = value(c[i], sx, a.wsc[(size_t)e * a.N + min(n0 + 4 * q + i, a.N - 1)]);
+          return v;
+        };
+        f32x4 v = values(u, first_row(f));
+        if constexpr (MODE == INT8_GATE_UP) {
+          const f32x4 up = values(u + R / 2 * NT, first_row(f + R / 2));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], up[i], a.limit);
+        }
+        const size_t orow = MODE == INT8_DOWN ? a.pairs[row] : row;
+        store4(a.out + orow * (size_t)a.ldo, slab * kItemN + 16 * f + 4 * q, nspan, v);
+      }
+    }
+    __syncthreads();  // the sums are read before the next item's overwrite them
+  }
+}
+
+// Grouped token tiles of `per` rows, at most: an expert's last one need not be full.
+long long most_tiles(const Int8Args& a, int per) {
+  return min((long long)a.rows, (long long)(a.rows + per - 1) / per + min(a.rows, a.E));
+}
+
+template <int NT, int R, int KS, int D, Int8Mode MODE, bool BLOCK>
+hipError_t launch_one(const Int8Args& a, int cus, hipStream_t s) {
+  const int span = MODE == INT8_GATE_UP ? a.N / 2 : a.N, per = MODE == INT8_GATE_UP ? 8 * R : 16 * R;
+  const long long slabs = (span + per - 1) / per;
+  const int kRows = BLOCK ? a.cap : 16 * NT;
+  const long long tiles = MODE == INT8_DENSE ? (a.rows + kRows - 1) / kRows : most_tiles(a, kRows);
+  long long grid = tiles * slabs;
+  // grouped (the number of items is known on the device only): as many as run at once
+  const long long most = MODE != INT8_DENSE ? 3LL * cus : 1LL << 20;
+  if (grid > most) grid = most;
+  size_t bytes = 0;
+  if constexpr (BLOCK) {
+    bytes = block_lds(a.cap, a.K);
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&int8_stream_kernel<NT, R, KS, D, MODE, BLOCK>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kBlockLds);
+    if (e != hipSuccess) return e;
+  }
+  int8_stream_kernel<NT, R, KS, D, MODE, BLOCK><<<dim3((unsigned)grid), dim3(64 * KS), bytes, s>>>(a);
+  return hipGetLastError();
+}
+
+template <Int8Mode MODE>
+hipError_t launch_grouped(const Int8Args& a, int cus, hipStream_t s) {
+  if (a.cap > 0) {
+    const long long slabs = MODE == INT8_GATE_UP ? (a.N / 2 + 31) / 32 : (a.N + 63) / 64;  // of 64 rows
+    return most_tiles(a, a.cap) * slabs <= 3LL * cus / 2 ? launch_one<1, 2, 4, 4, MODE, true>(a, cus, s)
+                                                         : launch_one<1, 4, 4, 2, MODE, true>(a, cus, s);
+  }
+  return a.rows <= 16LL * a.E ? launch_one<1, 4, 4, 2, MODE, false>(a, cus, s) : launch_one<2, 4, 4, 2, MODE, false>(a, cus, s);
+}
+
+}  // namespace
+
+bool int8_decode_fits(int M, int K) { return M <= 16 && M * (int8_pad(K) / 128) <= 224; }
+
+// A tile holds an expert's rows of up to 16 tokens where two blocks' codes fit a CU's LDS.
+int int8_block_rows(int T, int K) {
+  const int cap = min(T, 16);
+  return block_lds(cap, K) <= kBlockLds ? cap : 0;
+}
+
+hipError_t launch_int8_stream(Int8Mode mode, const Int8Args& a, int cus, hipStream_t s) {
+  switch (mode) {
+    case INT8_DENSE:
+      if (!a.xq) return launch_one<1, 1, 8, 2, INT8_DENSE, true>(a, cus, s);
+      if (a.rows > 16) return launch_one<2, 1, 16, 2, INT8_DENSE, false>(a, cus, s);
+      return a.K >= 32 * 128 ? launch_one<1, 1, 16, 2, INT8_DENSE, false>(a, cus, s)
+                             : launch_one<1, 2, 8, 2, INT8_DENSE, false>(a, cus, s);
+    case INT8_GATE_UP: return launch_grouped<INT8_GATE_UP>(a, cus, s);
+    default: return launch_grouped<INT8_DOWN>(a, cus, s);
+  }
+}
+
+}  // namespace moe

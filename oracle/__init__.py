@@ -35,4 +35,7 @@ Modules:
   linear  - dense NVFP4 linear layer
   fp8_block - products on block-128 fp8 weights, dense and over experts
   router  - balance loss, router z-loss and the logits' gradient
+  scored_routing - routing by scores (groups, choice bias) and its gradient
+  int8    - products on 8-bit integer weights, dense and over experts
+  block_end - weighted sum, shared expert, norms and residual, and their gradients
 """
