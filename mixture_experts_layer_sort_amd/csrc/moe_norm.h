@@ -32,10 +32,14 @@ struct NormArgs {
   float* part;               // workspace: [blocks][2][H]
 };
 
-// Blocks of the gradient's first launch: each adds its tokens' parts of the weights' gradients.
-constexpr int kNormBlocks = 512;
+// Blocks of the gradient's first launch, each of which adds its tokens' parts of the weights' gradients: as many as run
+// at once on 256 compute units of 8 waves (16 columns a thread).
+inline int norm_blocks(int T, int H) {
+  const int waves = (H + 1023) / 1024, most = 256 * (waves < 8 ? 8 / waves : 1);
+  return T < most ? T : most;
+}
 inline size_t norm_backward_bytes(int T, int H) {
-  const size_t n = (size_t)(T < kNormBlocks ? T : kNormBlocks) * 2 * H * sizeof(float);
+  const size_t n = (size_t)norm_blocks(T, H) * 2 * H * sizeof(float);
   return (n + 255) / 256 * 256;
 }
 

@@ -204,3 +204,5 @@ def test_norm_gradient_workspace():
     assert f(0, 64) == 0 and f(5, 60) == 0 and f(5, 16392) == 0 and f((1 << 24) + 1, 64) == 0
     sizes = [f(T, 64) for T in (1, 2, 100, 255, 256, 257, 511, 512, 513, 5000, 1 << 20)]
     assert sizes == sorted(sizes) and sizes[0] > 0
+    for H in (8, 16, 504, 512, 520, 1024, 2048, 8192, 8200, 16384):  # both norms' parts of every block
+        assert f(1, H) >= 8 * H and f(1 << 20, H) >= 256 * 8 * H, H
