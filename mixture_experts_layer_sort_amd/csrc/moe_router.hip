@@ -7,14 +7,18 @@
 //   w_j = scale s_j / (sum_i s_i or 1)
 //
 // Which of two experts is picked can hang on the last bit of a score, so scores
-// are computed in 64 bits (relative error below 1e-14) and rounded once to the
+// are computed in 64 bits (relative error below 3e-14) and rounded once to the
 // 32 bits that the definition names: picks are the same whatever computes them.
+// (On this GPU a 64-bit multiply-add issues like a 32-bit one.)
 //
 // A token has L lanes, a lane V consecutive experts, so that positions order
-// like ids and equal choices need no ids to be compared: a round takes the
-// maximum of the lanes' maxima, and the first lane that has it takes its first
-// expert that has it.  L = 16 (four tokens per wave share every exchange) where
-// there are tokens enough to fill the GPU, L = 64 for few tokens or many experts.
+// like ids and equal choices need no ids to be compared.  A lane sorts its largest
+// KEEP >= min(k, V) choices (keys alone, by a network); a round takes the maximum of
+// the lanes' first keys, and the first lane that has it moves its list up by one.
+// Which expert of the lane it was is looked up at the end for all picks at once,
+// in the keys as they were (picks of one lane with one value follow each other, the
+// n-th is the n-th such expert).  L = 16 (four tokens per wave share every exchange)
+// where there are tokens enough to fill the GPU, L = 64 for few tokens or many experts.
 #include "moe_router.h"
 
 #include "moe_wave.h"
@@ -23,43 +27,47 @@ namespace moe {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kMaxK = 32;
 constexpr uint32_t kOff = 0x007FFFFFu;  // key of -inf: still before 0, an expert that cannot be picked
 
-// exp(x) for x <= 709.78, to 1e-14: 2^n times the Taylor sum of the rest, |rest| <= ln 2 / 2 (12th term: 6e-15).
-__device__ __forceinline__ double exp64(double x) {
-  if (x < -745.0) return 0.0;  // NaN goes on
-  const double n = rint(x * 1.4426950408889634074);
-  const double f = fma(n, -1.9082149292705877e-10, fma(n, -0.69314718036912381649, x));  // ln 2 in two parts
-  double p = 1.0 / 39916800.0;
-  p = fma(p, f, 1.0 / 3628800.0);
-  p = fma(p, f, 1.0 / 362880.0);
-  p = fma(p, f, 1.0 / 40320.0);
-  p = fma(p, f, 1.0 / 5040.0);
-  p = fma(p, f, 1.0 / 720.0);
-  p = fma(p, f, 1.0 / 120.0);
-  p = fma(p, f, 1.0 / 24.0);
-  p = fma(p, f, 1.0 / 6.0);
-  p = fma(p, f, 0.5);
-  p = fma(p, f, 1.0);
-  p = fma(p, f, 1.0);
-  return ldexp(p, (int)n);
-}
+// exp(x), |x| <= 709: 2^n times a polynomial of the rest f, |f| <= ln 2 / 2 (interpolated at the 10 Chebyshev nodes, off
+// by 2e-14 relative; with ln 2 in one part another 1e-16 |n| / 2).
+// Constants come from scalar registers (one instruction a step; as literals each would be moved into place first), n by
+// an addition that leaves it in the low bits of 1.5 2^52 + n, and 2^n by an addition to the exponent.
+struct Exp64 {
+  double c[10], log2e, ln2, round;
+  __device__ __forceinline__ Exp64()
+      : c{1.0000000000000135,    1.0000000000000013,    0.4999999999943859,     0.16666666666615648,    0.04166666704055213,
+          0.008333333367311624,  0.0013888801749621653, 0.00019841190647512536, 2.4884459768350122e-05, 2.763264069051338e-06},
+        log2e(1.4426950408889634074), ln2(-0.69314718055994530942), round(0x1.8p52) {
+#pragma unroll
+    for (int i = 0; i < 10; ++i) asm("" : "+s"(c[i]));
+    asm("" : "+s"(log2e), "+s"(ln2), "+s"(round));
+  }
+  __device__ __forceinline__ double operator()(double x) const {
+    const double y = fma(x, log2e, round), f = fma(y - round, ln2, x);
+    double p = c[9];
+#pragma unroll
+    for (int i = 8; i >= 0; --i) p = fma(p, f, c[i]);
+    return __hiloint2double(__double2hiint(p) + (__double2loint(y) << 20), __double2loint(p));
+  }
+};
+// exp(x), x <= 709; 0 below -700.  NaN goes on: the sum of exponents leaves one as it is or makes a number of it.
+__device__ __forceinline__ double exp64(double x, const Exp64& e) { return x < -700.0 ? 0.0 : x == x ? e(x) : x; }
 
-// 1 / d, d a normal number: the hardware's estimate and two Newton steps.
+// 1 / d, d a normal number: the hardware's estimate r and its error's series, r (1 + e + e^2), e = 1 - d r.
 __device__ __forceinline__ double rcp64(double d) {
-  double r = __builtin_amdgcn_rcp(d);
-  r = fma(fma(-d, r, 1.0), r, r);
-  return fma(fma(-d, r, 1.0), r, r);
+  const double r = __builtin_amdgcn_rcp(d), e = fma(-d, r, 1.0);
+  return fma(r, fma(e, e, e), r);
 }
 
-// Keys in LDS: a word is left out after every 32, so that groups of 32 begin in different banks.
-__host__ __device__ constexpr int key_at(int e) { return e + (e >> 5); }
-
-// 0 below -709, where exp(-l) ends.
-__device__ __forceinline__ double sigmoid64(float l) {
-  if (l < -709.f) return 0.0;
-  return rcp64(1.0 + exp64(-(double)l));
+// 0 below -700, where exp(-l) nears the end of 64 bits.
+__device__ __forceinline__ double sigmoid64(float l, const Exp64& e) {
+  if (l < -700.f) return 0.0;
+  return rcp64(1.0 + exp64(-(double)l, e));
+}
+// The same rounded to 32 bits (0 below -104); l = NaN: unspecified.
+__device__ __forceinline__ float sigmoid32(float l, const Exp64& e) {
+  return (float)rcp64(1.0 + e((double)fminf(fmaxf(-l, -700.f), 700.f)));
 }
 
 // Order of fp32 values as unsigned numbers (-0 is 0); NaN is with -inf.
@@ -72,33 +80,122 @@ __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-template <int L, int V, bool SOFTMAX, bool VEC>
+// ------------------------------------------------------------------ sorting a lane's keys, largest first
+
+template <int N>
+__device__ __forceinline__ void exchange(uint32_t (&v)[N], int i, int j) {
+  const uint32_t a = v[i], b = v[j];
+  v[i] = max(a, b);
+  v[j] = min(a, b);
+}
+// Merge exchange sort (Batcher) of v[lo .. lo + n), n a power of two, by its loops over p, q, r, d.
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&v)[N], int lo, int n) {
+#pragma unroll
+  for (int p = 1; p < n; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < n; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < n && (i + j) / (2 * p) == (i + j + k) / (2 * p)) exchange(v, lo + i + j, lo + i + j + k);
+}
+// The largest KEEP of key, sorted.
+template <int V, int KEEP>
+__device__ __forceinline__ void sort_list(const uint32_t (&key)[V], uint32_t (&list)[KEEP]) {
+  uint32_t v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = key[i];
+  if constexpr (KEEP == V) {
+    sort_keys<V>(v, 0, V);
+  } else {  // both halves, the larger of opposite places (the largest half, first rising, then falling), and its merge
+    static_assert(2 * KEEP == V, "half");
+    sort_keys<V>(v, 0, KEEP);
+    sort_keys<V>(v, KEEP, KEEP);
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) v[i] = max(v[i], v[V - 1 - i]);
+#pragma unroll
+    for (int d = KEEP / 2; d >= 1; d /= 2)
+#pragma unroll
+      for (int i = 0; i < KEEP; ++i)
+        if ((i & d) == 0) exchange(v, i, i + d);
+  }
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) list[i] = v[i];
+}
+
+// ------------------------------------------------------------------ groups
+
+// The two largest keys of a group that has its LG lanes in a row (LG a power of two up to 16), in each of them.
+template <int D>
+__device__ __forceinline__ void join_two(uint32_t& b1, uint32_t& b2) {
+  uint32_t o1, o2;
+  if constexpr (D == 1) {         // lane ^ 1, ^ 2: within four lanes
+    o1 = __builtin_amdgcn_update_dpp(0u, b1, 0xB1, 0xF, 0xF, true);
+    o2 = __builtin_amdgcn_update_dpp(0u, b2, 0xB1, 0xF, 0xF, true);
+  } else if constexpr (D == 2) {
+    o1 = __builtin_amdgcn_update_dpp(0u, b1, 0x4E, 0xF, 0xF, true);
+    o2 = __builtin_amdgcn_update_dpp(0u, b2, 0x4E, 0xF, 0xF, true);
+  } else if constexpr (D == 4) {  // mirrored in eight: fours are equal by now
+    o1 = __builtin_amdgcn_update_dpp(0u, b1, 0x141, 0xF, 0xF, true);
+    o2 = __builtin_amdgcn_update_dpp(0u, b2, 0x141, 0xF, 0xF, true);
+  } else {
+    o1 = ror16<8>(b1);
+    o2 = ror16<8>(b2);
+  }
+  b2 = max(min(b1, o1), max(b2, o2));
+  b1 = max(b1, o1);
+}
+
+// Groups of LG whole lanes before this lane's (with a larger score, or as large and lower).
+template <int R>
+__device__ __forceinline__ void count_before(uint32_t score, int sub, int LG, int& before) {
+  if constexpr (R < 16) {
+    if ((R & (LG - 1)) == 0) {  // rotated by whole groups: a lower one comes from R lanes below, if there are any
+      const uint32_t other = ror16<R>(score);
+      before += other > score || (other == score && sub >= R);
+    }
+    count_before<R + 1>(score, sub, LG, before);
+  }
+}
+
+template <int L, int V, int KEEP, bool SOFTMAX, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouterArgs a) {
   constexpr int TW = 64 / L;  // tokens of a wave
-  extern __shared__ __align__(16) uint32_t shared[];  // groups: keys [wave][TW][key_words], scores [wave][TW][G]
-  __shared__ int picks[kWaves][TW][kMaxK];
+  __shared__ uint32_t shared[kWaves * TW][V * L];  // keys: expert sub V + i at i L + sub
+  extern __shared__ uint32_t scores[];             // groups that are not whole lanes: [wave][TW][G]
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int sub = lane & (L - 1), slot = lane / L;
   const long long t = ((long long)blockIdx.x * kWaves + wv) * TW + slot;
   const float* row = a.logits + min(t, (long long)a.T - 1) * a.ldl;
+  uint32_t* keys = shared[wv * TW + slot];
   const int e0 = sub * V;
 
-  float l[V];
+  float l[V], b[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) l[i] = -INFINITY;
+  for (int i = 0; i < V; ++i) l[i] = -INFINITY, b[i] = 0.f;
   if constexpr (VEC) {
 #pragma unroll
     for (int i = 0; i < V; i += 4)
       if (e0 + i < a.E) {
         const float4 v = *reinterpret_cast<const float4*>(row + e0 + i);
         l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
+        if (a.bias) {
+          const float4 c = *reinterpret_cast<const float4*>(a.bias + e0 + i);
+          b[i] = c.x, b[i + 1] = c.y, b[i + 2] = c.z, b[i + 3] = c.w;
+        }
       }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (e0 + i < a.E) l[i] = row[e0 + i];
+      if (e0 + i < a.E) {
+        l[i] = row[e0 + i];
+        if (a.bias) b[i] = a.bias[e0 + i];
+      }
   }
 
+  const Exp64 ex64;
   double top = 0.0, inv = 1.0;  // softmax: largest logit, 1 / sum
   uint32_t key[V];
   if constexpr (SOFTMAX) {
@@ -109,85 +206,111 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouterArgs a)
     top = m == -INFINITY ? 0.0 : (double)m;  // every expert is off: all scores are 0
     double ex[V], sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += ex[i] = exp64((double)l[i] - top);
+    for (int i = 0; i < V; ++i) sum += ex[i] = exp64((double)l[i] - top, ex64);
     sum = sum_lanes<L>(sum);
     inv = sum == 0.0 ? 0.0 : rcp64(sum);
 #pragma unroll
     for (int i = 0; i < V; ++i) key[i] = __float_as_uint((float)(ex[i] * inv));
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = __float_as_uint((float)sigmoid64(l[i]));
+    for (int i = 0; i < V; ++i) key[i] = __float_as_uint(sigmoid32(l[i], ex64));
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = e0 + i;
-    const float b = a.bias ? a.bias[min(e, a.E - 1)] : 0.f;
-    const uint32_t k = l[i] == -INFINITY ? kOff : order_key(__uint_as_float(key[i]) + b);
-    key[i] = e < a.E ? k : 0u;
+    const uint32_t k = l[i] == -INFINITY ? kOff : order_key(__uint_as_float(key[i]) + b[i]);
+    key[i] = e0 + i < a.E ? k : 0u;
+    keys[i * L + sub] = key[i];
   }
+  uint32_t list[KEEP];
+  sort_list<V, KEEP>(key, list);
 
-  if (a.KG < a.G) {  // experts of groups that are not kept: 0
-    const int per = a.E / a.G;
-    const int words = key_at(a.E);
-    uint32_t* keys = shared + (wv * TW + slot) * words;
-    uint32_t* score = shared + kWaves * TW * words + (wv * TW + slot) * a.G;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (e0 + i < a.E) keys[key_at(e0 + i)] = key[i];
-    wave_lds_sync();
-    for (int g = sub; g < a.G; g += L) {
-      uint32_t b1 = 0, b2 = 0;
-      for (int i = 0; i < per; ++i) {
-        const uint32_t k = keys[key_at(g * per + i)];
-        b2 = max(b2, min(b1, k));
-        b1 = max(b1, k);
-      }
-      score[g] = a.top == 1 ? b1 : order_key(of_key(b1) + of_key(b2));
-    }
-    wave_lds_sync();
-    for (int g = sub; g < a.G; g += L) {
-      const uint32_t mine = score[g];
+  if (a.KG < a.G) {  // lists of experts of groups that are not kept: 0
+    const int per = a.E / a.G, LG = per / V;
+    if (LG * V == per && LG <= 16 && (LG & (LG - 1)) == 0) {
+      uint32_t b1 = list[0], b2 = KEEP > 1 ? list[KEEP > 1 ? 1 : 0] : 0u;
+      if (LG > 1) join_two<1>(b1, b2);
+      if (LG > 2) join_two<2>(b1, b2);
+      if (LG > 4) join_two<4>(b1, b2);
+      if (LG > 8) join_two<8>(b1, b2);
+      uint32_t score = a.top == 1 ? b1 : order_key(of_key(b1) + of_key(b2));
       int before = 0;
-      for (int h = 0; h < a.G; ++h) {
-        const uint32_t other = score[h];
-        before += other > mine || (other == mine && h < g);
+      if constexpr (L == 16) {
+        score = e0 < a.E ? score : 0u;  // lanes behind the last expert: behind every group
+        count_before<1>(score, sub, LG, before);
+      } else {
+        for (int g = 0; g < a.G; ++g) {
+          const uint32_t other = __builtin_amdgcn_readlane(score, g * LG);
+          before += other > score || (other == score && g * LG < (sub & -LG));
+        }
       }
-      if (before >= a.KG)
-        for (int i = 0; i < per; ++i) keys[key_at(g * per + i)] = 0u;
-    }
-    wave_lds_sync();
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = e0 + i < a.E ? keys[key_at(e0 + i)] : 0u;
+      for (int i = 0; i < KEEP; ++i) list[i] = before < a.KG ? list[i] : 0u;
+    } else {
+      uint32_t* score = scores + (wv * TW + slot) * a.G;
+      wave_lds_sync();
+      for (int g = sub; g < a.G; g += L) {
+        uint32_t b1 = 0, b2 = 0;
+        for (int e = g * per; e < (g + 1) * per; ++e) {
+          const uint32_t k = keys[e % V * L + e / V];
+          b2 = max(b2, min(b1, k));
+          b1 = max(b1, k);
+        }
+        score[g] = a.top == 1 ? b1 : order_key(of_key(b1) + of_key(b2));
+      }
+      wave_lds_sync();
+      for (int g = sub; g < a.G; g += L) {
+        const uint32_t mine = score[g];
+        int before = 0;
+        for (int h = 0; h < a.G; ++h) {
+          const uint32_t other = score[h];
+          before += other > mine || (other == mine && h < g);
+        }
+        if (before >= a.KG)
+          for (int e = g * per; e < (g + 1) * per; ++e) keys[e % V * L + e / V] = 0u;
+      }
+      wave_lds_sync();
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = keys[i * L + sub];
+      sort_list<V, KEEP>(key, list);
+    }
   }
 
+  // round j: its value, lane, and how many before it had both
+  uint32_t value = 0, last = 0;
+  int from = 0, nth = 0, last_lane = -1, run = 0;
   for (int j = 0; j < a.k; ++j) {
-    uint32_t m = key[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) m = max(m, key[i]);
-    const uint32_t best = max_lanes<L>(m);
-    const uint64_t same = __ballot(m == best);
+    const uint32_t best = max_lanes<L>(list[0]);
+    const uint64_t same = __ballot(list[0] == best);
     int first;
     if constexpr (L == 64) first = __ffsll((unsigned long long)same) - 1;
     else first = __ffs((uint32_t)(same >> (lane & 48)) & 0xFFFFu) - 1;
-    int at = 0;
-    bool open = sub == first;
+    run = best == last && first == last_lane ? run + 1 : 0;
+    last = best;
+    last_lane = first;
+    value = sub == j ? best : value;
+    from = sub == j ? first : from;
+    nth = sub == j ? run : nth;
+    // by a bit mask (as a choice of values it compiles to selects among all places)
+    const uint32_t move = sub == first ? ~0u : 0u;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const bool hit = open && key[i] == best;
-      at = hit ? i : at;
-      key[i] = hit ? 0u : key[i];
-      open = open && !hit;
-    }
-    if (sub == first) picks[wv][slot][j] = e0 + at;
+    for (int i = 0; i < KEEP; ++i) list[i] ^= (list[i] ^ (i + 1 < KEEP ? list[i + 1 < KEEP ? i + 1 : i] : 0u)) & move;
   }
   wave_lds_sync();
+  int at = 0;
+#pragma unroll
+  for (int i = V - 1; i >= 0; --i) at = keys[i * L + from] == value ? i : at;  // the first one
+  if (nth > 0) {
+    int seen = 0;
+    for (int i = 0; i < V; ++i)
+      if (keys[i * L + from] == value && seen++ == nth) at = i;
+  }
 
   const bool mine = sub < a.k;
-  const int id = mine ? picks[wv][slot][sub] : 0;
+  const int id = mine ? from * V + at : 0;
   double s = 0.0;
   if (mine) {
     const float z = row[id];
-    s = SOFTMAX ? exp64((double)z - top) * inv : sigmoid64(z);
+    s = SOFTMAX ? exp64((double)z - top, ex64) * inv : sigmoid64(z, ex64);
   }
   if (a.renorm) {
     const double sum = sum_lanes<L>(s);
@@ -199,12 +322,21 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouterArgs a)
   }
 }
 
+// exp(x) for x <= 0 to 2^-22: the exponent's whole and broken part in 64 bits (a difference of two logits has no rounding
+// there), the power of the broken part in 32.
+__device__ __forceinline__ float exp_diff(float z, double m) {
+  const double x = ((double)z - m) * 1.4426950408889634074, n = rint(x);
+  const float p = ldexpf(__builtin_amdgcn_exp2f((float)(x - n)), (int)n);
+  return x < -200.0 ? 0.f : p;  // NaN goes on
+}
+
 // Gradient.  L lanes per token; lane j has pick j and its part of the gradient in 64 bits; the parts meet the row's
-// other values in LDS, where a lane has the experts 4 (l + L i) .. + 3 (or l + L i), so that rows are stored in one run.
-// Only softmax scores that are not renormalised give every expert a gradient; else the logits are read at the picks only.
-template <int L, bool VEC>
+// other values in LDS, where a lane has 16 experts in fours (4 (l + L i) .. + 3) or, unaligned, every L-th, so that rows
+// are stored in one run.  DENSE: softmax scores that are not renormalised, which give every expert a gradient; else the
+// logits are read at the picks only, and the rest of a row is zero.
+template <int L, bool DENSE, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(RouterArgs a) {
-  constexpr int TW = 64 / L;
+  constexpr int TW = 64 / L, N = 16;
   extern __shared__ __align__(16) float rows[];  // [wave][TW][E rounded up to 4]
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int sub = lane & (L - 1), slot = lane / L;
@@ -213,7 +345,22 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
   const float* row = a.logits + tt * a.ldl;
   float* mine = rows + (size_t)(wv * TW + slot) * ((a.E + 3) / 4 * 4);
   const bool keep = t < a.T && (!a.mask || a.mask[tt]);
-  const bool dense = a.softmax && !a.renorm;
+  auto expert = [&](int i) { return VEC ? 4 * (sub + L * (i / 4)) + i % 4 : sub + L * i; };
+
+  float p[N];  // DENSE: logits, then their exponentials
+  if constexpr (DENSE) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      if constexpr (VEC) {
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (expert(i) < a.E) v = *reinterpret_cast<const float4*>(row + expert(i));
+        p[i] = v.x, p[i + 1] = v.y, p[i + 2] = v.z, p[i + 3] = v.w;
+      } else {
+#pragma unroll
+        for (int c = i; c < i + 4; ++c) p[c] = expert(c) < a.E ? row[expert(c)] : -INFINITY;
+      }
+    }
+  }
 
   // picks (an id outside [0, E) has no part)
   int id = -1;
@@ -228,33 +375,34 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
     }
   }
   float m = id >= 0 ? z : -INFINITY;
-  float dot = 0.f, inv = 0.f;
-  if (dense) {
-    for (int e = sub; e < a.E; e += L) m = fmaxf(m, row[e]);
+  if constexpr (DENSE) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = fmaxf(m, p[i]);
   }
   m = max_lanes<L>(m);
   if (m == -INFINITY) m = 0.f;
+  const Exp64 ex64;
   double s = 0.0, ds = 0.0;  // score, and its derivative by its own logit (softmax: the first term)
   if (id >= 0) {
     if (a.softmax) {
-      ds = s = exp64((double)z - m);
+      ds = s = exp64((double)z - m, ex64);
     } else {
-      const double e = exp64(-fabs((double)z)), r = rcp64(1.0 + e);
+      const double e = exp64(-fabs((double)z), ex64), r = rcp64(1.0 + e);
       s = z < 0.f ? e * r : r;
       ds = e * r * r;
     }
   }
   double part;
-  if (dense) {
-    // sum of all experts' exponentials in the order of the lanes; the row's own terms below in 32 bits
+  if constexpr (DENSE) {
     double sum = 0.0;
-    for (int e = sub; e < a.E; e += L) sum += exp64((double)row[e] - m);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += p[i] = exp_diff(p[i], m);
     sum = sum_lanes<L>(sum);
     const double is = sum == 0.0 ? 0.0 : rcp64(sum);
-    s *= is;
-    dot = (float)sum_lanes<L>(g * s);
-    inv = (float)is;
-    part = g * s;
+    part = g * s * is;
+    const float f = (float)(-sum_lanes<L>(part) * is);
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] *= f;
   } else {
     if (a.renorm) {
       const double sum = sum_lanes<L>(s);
@@ -262,60 +410,88 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
       g = (g - sum_lanes<L>(g * s) * is) * is;
     }
     part = g * ds;
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = 0.f;
   }
 
-  for (int e = sub; e < a.E; e += L)
-    mine[e] = dense ? -dot * inv * (float)exp64((double)row[e] - m) : 0.f;
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    if constexpr (VEC) {
+      if (expert(i) < a.E) *reinterpret_cast<float4*>(mine + expert(i)) = make_float4(p[i], p[i + 1], p[i + 2], p[i + 3]);
+    } else {
+#pragma unroll
+      for (int c = i; c < i + 4; ++c)
+        if (expert(c) < a.E) mine[expert(c)] = p[c];
+    }
+  }
   wave_lds_sync();
   if (id >= 0) atomicAdd(&mine[id], (float)part);
   wave_lds_sync();
   if (t >= a.T) return;
   float* out = a.d_logits + t * a.ldd;
-  if constexpr (VEC) {
-    for (int e = 4 * sub; e < a.E; e += 4 * L) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    if constexpr (VEC) {
+      const int e = expert(i);
+      if (e >= a.E) break;
       float4 v = keep ? *reinterpret_cast<const float4*>(mine + e) : make_float4(0.f, 0.f, 0.f, 0.f);
       if (a.accumulate) {
         const float4 o = *reinterpret_cast<const float4*>(out + e);
         v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
       }
       *reinterpret_cast<float4*>(out + e) = v;
-    }
-  } else {
-    for (int e = sub; e < a.E; e += L) {
-      const float v = keep ? mine[e] : 0.f;
-      out[e] = a.accumulate ? out[e] + v : v;
+    } else {
+#pragma unroll
+      for (int c = i; c < i + 4; ++c) {
+        const int e = expert(c);
+        if (e >= a.E) break;
+        const float v = keep ? mine[e] : 0.f;
+        out[e] = a.accumulate ? out[e] + v : v;
+      }
     }
   }
 }
 
 bool vec4(const void* p, long long ld, int E) { return E % 4 == 0 && ld % 4 == 0 && ((uintptr_t)p & 15) == 0; }
 
-template <int L, int V>
-hipError_t launch_forward(const RouterArgs& a, hipStream_t s) {
+template <int L, int V, int KEEP>
+hipError_t launch_lists(const RouterArgs& a, hipStream_t s) {
   constexpr int per = kWaves * (64 / L);
   const dim3 grid((unsigned)(((long long)a.T + per - 1) / per)), block(64 * kWaves);
-  const size_t lds = a.KG < a.G ? (size_t)per * (key_at(a.E) + a.G) * 4 : 0;
-  const bool vec = V % 4 == 0 && vec4(a.logits, a.ldl, a.E);
+  const size_t lds = a.KG < a.G ? (size_t)per * a.G * 4 : 0;
   if constexpr (V % 4 == 0) {
-    if (vec) {
-      if (a.softmax) route_scores_kernel<L, V, true, true><<<grid, block, lds, s>>>(a);
-      else route_scores_kernel<L, V, false, true><<<grid, block, lds, s>>>(a);
+    if (vec4(a.logits, a.ldl, a.E) && ((uintptr_t)a.bias & 15) == 0) {
+      if (a.softmax) route_scores_kernel<L, V, KEEP, true, true><<<grid, block, lds, s>>>(a);
+      else route_scores_kernel<L, V, KEEP, false, true><<<grid, block, lds, s>>>(a);
       return hipGetLastError();
     }
   }
-  if (a.softmax) route_scores_kernel<L, V, true, false><<<grid, block, lds, s>>>(a);
-  else route_scores_kernel<L, V, false, false><<<grid, block, lds, s>>>(a);
+  if (a.softmax) route_scores_kernel<L, V, KEEP, true, false><<<grid, block, lds, s>>>(a);
+  else route_scores_kernel<L, V, KEEP, false, false><<<grid, block, lds, s>>>(a);
   return hipGetLastError();
 }
+template <int L, int V>
+hipError_t launch_forward(const RouterArgs& a, hipStream_t s) {
+  if constexpr (V == 16) {
+    if (a.k <= 8) return launch_lists<L, 16, 8>(a, s);
+  }
+  return launch_lists<L, V, V>(a, s);
+}
 
-template <int L>
-hipError_t launch_backward(const RouterArgs& a, hipStream_t s) {
+template <int L, bool DENSE>
+hipError_t launch_rows(const RouterArgs& a, hipStream_t s) {
   constexpr int per = kWaves * (64 / L);
   const dim3 grid((unsigned)(((long long)a.T + per - 1) / per)), block(64 * kWaves);
   const size_t lds = (size_t)per * ((a.E + 3) / 4 * 4) * 4;
-  if (vec4(a.d_logits, a.ldd, a.E)) route_scores_backward_kernel<L, true><<<grid, block, lds, s>>>(a);
-  else route_scores_backward_kernel<L, false><<<grid, block, lds, s>>>(a);
+  if (vec4(a.d_logits, a.ldd, a.E) && (!DENSE || vec4(a.logits, a.ldl, a.E)))
+    route_scores_backward_kernel<L, DENSE, true><<<grid, block, lds, s>>>(a);
+  else
+    route_scores_backward_kernel<L, DENSE, false><<<grid, block, lds, s>>>(a);
   return hipGetLastError();
+}
+template <int L>
+hipError_t launch_backward(const RouterArgs& a, hipStream_t s) {
+  return a.softmax && !a.renorm ? launch_rows<L, true>(a, s) : launch_rows<L, false>(a, s);
 }
 
 // Few tokens: a wave each, for the shorter chain; more than there are waves for: 16 lanes each.  16 lanes hold up to

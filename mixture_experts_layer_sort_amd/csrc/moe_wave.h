@@ -16,7 +16,7 @@ __device__ __forceinline__ void wave_lds_sync() {
 }
 
 template <int N>
-__device__ __forceinline__ uint32_t ror16(uint32_t v) {  // the value of lane l + N of the same row of 16, round
+__device__ __forceinline__ uint32_t ror16(uint32_t v) {  // the value of lane l - N of the same row of 16, round
   return __builtin_amdgcn_update_dpp(0u, v, 0x120 + N, 0xF, 0xF, true);
 }
 template <int N>

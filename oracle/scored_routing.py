@@ -13,7 +13,7 @@ def scores(row, kind):
     row = np.asarray(row, np.float64)
     with np.errstate(over="ignore", invalid="ignore"):
         if kind == "sigmoid":
-            return np.array([1.0 / (1.0 + np.exp(-v)) if v >= -709 else 0.0 for v in row])
+            return np.array([1.0 / (1.0 + np.exp(-v)) if v >= -700 else 0.0 for v in row])
         m = row.max()
         if m == -np.inf:
             return np.zeros_like(row)
