@@ -217,6 +217,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouterArgs a)
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
+    asm("" : "+v"(key[i]));  // computed for all: not sunk behind a branch for experts that are off, one by one
     const uint32_t k = l[i] == -INFINITY ? kOff : order_key(__uint_as_float(key[i]) + b[i]);
     key[i] = e0 + i < a.E ? k : 0u;
     keys[i * L + sub] = key[i];
@@ -494,9 +495,10 @@ hipError_t launch_backward(const RouterArgs& a, hipStream_t s) {
   return a.softmax && !a.renorm ? launch_rows<L, true>(a, s) : launch_rows<L, false>(a, s);
 }
 
-// Few tokens: a wave each, for the shorter chain; more than there are waves for: 16 lanes each.  16 lanes hold up to
-// 256 experts and 16 picks.
-bool sixteen(const RouterArgs& a) { return a.T > 2048 && a.E <= 256 && a.k <= 16; }
+// A wave for each of few tokens, for the shorter chain; 16 lanes where tokens fill the GPU that way (sigmoid, top-8, us
+// with 64 / 16 lanes: 256 experts, 2048 tokens 5.2 / 6.4, 4096 6.6 / 6.5, 16384 17.9 / 12.2; 64 experts, 2048 tokens
+// 3.4 / 3.6, 4096 4.1 / 3.7).  16 lanes hold up to 256 experts and 16 picks.
+bool sixteen(const RouterArgs& a) { return a.T > (a.E > 128 ? 4096 : 2048) && a.E <= 256 && a.k <= 16; }
 
 }  // namespace
 
