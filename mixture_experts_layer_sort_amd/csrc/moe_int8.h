@@ -56,11 +56,18 @@ __device__ __forceinline__ void int8_factor(float m, float& f, float& s) {
   s = ok ? m / kInt8Max : __uint_as_float(0x7FC00000u);
 }
 
-// Codes of 4 and 8 values under the factor f: magnitudes are at most 127 (1 + 2^-23), which rounds to 127.  A value that
-// is not finite has f = 0: its product is NaN, whose conversion is 0.
+// Codes of 4 and 8 values under the factor f: magnitudes are at most 127 (1 + 2^-23), which rounds to 127.  Added to 1.5
+// 2^23 a value is rounded to its integer (ties to even), which is the sum's last byte then.  A value that is not finite
+// has f = 0: its product is the quiet NaN, whose last byte is 0.
 __device__ __forceinline__ uint32_t int8_codes4(float a, float b, float c, float d) {
-  const int i0 = (int)rintf(a), i1 = (int)rintf(b), i2 = (int)rintf(c), i3 = (int)rintf(d);
-  return (uint32_t)(i0 & 0xFF) | (uint32_t)(i1 & 0xFF) << 8 | (uint32_t)(i2 & 0xFF) << 16 | (uint32_t)i3 << 24;
+#pragma clang fp contract(off)  // a value is rounded before the addition: not one fused operation with the product
+  constexpr float kRound = 12582912.f;
+  auto bits = [](float v) {
+#pragma clang fp contract(off)
+    return __float_as_uint(v + kRound);
+  };
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(bits(d), bits(c), 0x0C0C0400u),
+                               __builtin_amdgcn_perm(bits(b), bits(a), 0x0C0C0400u), 0x05040100u);
 }
 __device__ __forceinline__ uint2 int8_codes8(const u32x4& v, float f) {
   return make_uint2(int8_codes4(bf16_lo(v[0]) * f, bf16_hi(v[0]) * f, bf16_lo(v[1]) * f, bf16_hi(v[1]) * f),
@@ -89,7 +96,7 @@ hipError_t launch_int8_quantize_tokens(int T, int K, const uint16_t* x, int8_t* 
 // The streaming kernel (few token rows per weight matrix): reads codes, or where a.cap > 0 (grouped) and
 // int8_decode_fits() (DENSE with xq null) quantises the rows itself.
 bool int8_decode_fits(int M, int K);
-int int8_block_rows(int T, int K);
+int int8_block_rows(Int8Mode mode, const Int8Args& a, int T, int cus);  // Int8Args::cap of T tokens, 0: codes
 hipError_t launch_int8_stream(Int8Mode mode, const Int8Args& a, int cus, hipStream_t s);
 // The tiled kernel (reads codes).  Grouped modes: `tile` sorted rows per token tile, token_tiles: at least their number.
 hipError_t launch_int8_tile(Int8Mode mode, const Int8Args& a, int tile, long long token_tiles, int cus, hipStream_t s);

@@ -8,6 +8,7 @@
 // holds does not matter, since tokens use the same order), D steps ahead.  The
 // waves' integer sums meet in LDS.
 #include "moe_int8.h"
+#include "moe_wave.h"
 
 namespace moe {
 namespace {
@@ -35,55 +36,63 @@ constexpr int kBlockLds = 64 * 1024;
 __host__ __device__ inline size_t block_lds(int rows, int K) { return (size_t)rows * (int8_pad(K) + 16); }
 
 // Rows `row(i)`, i < rows <= 16, of K bf16 values into LDS: codes [rows][Kp + 16] (the 16 rows of a fragment read start 4
-// banks apart), scales [rows].  Pieces of 8 values, 16 consecutive lanes in one row; the first HELD of a thread stay in
-// registers between the maximum and the codes, the others are read again.
-template <int HELD, class F>
-__device__ __forceinline__ void quantize_block(uint8_t* codes, float* scales, uint32_t* amax, int rows, int K, int tid,
-                                               int threads, F&& row) {
-  const int Kp = int8_pad(K), per = Kp / 8, n = rows * per;
-  const u32x4 none = {0, 0, 0, 0};
-  if (tid < 16) amax[tid] = __float_as_uint(kFp8Tiny);
+// banks apart), scales [rows].  G waves share a row (all KS of them one row, one each of KS or more).  A thread's first
+// HELD pieces of 8 values are loaded by load() (before the weights, since loads return in order) and stay in registers
+// between the maximum and the codes, the others are read again.
+template <int KS, int HELD, class F>
+struct BlockQuantizer {
+  int rows, K, G, wv, lane;
+  F row;
   u32x4 v[HELD];
-#pragma unroll
-  for (int u = 0; u < HELD; ++u) {
-    const int c = tid + u * threads, i = c / per, col = 8 * (c - i * per);
-    v[u] = c < n && col < K ? *reinterpret_cast<const u32x4*>(row(i) + col) : none;
+
+  __device__ __forceinline__ BlockQuantizer(int rows_, int K_, int wv_, int lane_, F row_)
+      : rows(rows_), K(K_), G(KS), wv(wv_), lane(lane_), row(row_) {
+    while (G > 1 && KS / G < rows) G /= 2;
   }
-  __syncthreads();
-  auto top = [&](int c, const u32x4& x) {
-    const uint32_t m = fp8_amax8(x, kFp8TinyBits);
-    // magnitudes on their bits, so that a NaN, above everything, stays
-    uint32_t b = max(m << 16, m & 0xFFFF0000u);
-    b = max(b, __builtin_amdgcn_update_dpp(0u, b, 0x128, 0xF, 0xF, true));
-    b = max(b, __builtin_amdgcn_update_dpp(0u, b, 0x124, 0xF, 0xF, true));
-    b = max(b, __builtin_amdgcn_update_dpp(0u, b, 0x122, 0xF, 0xF, true));
-    b = max(b, __builtin_amdgcn_update_dpp(0u, b, 0x121, 0xF, 0xF, true));
-    if ((tid & 15) == 0) atomicMax(&amax[c / per], b);
-  };
-#pragma unroll
-  for (int u = 0; u < HELD; ++u)
-    if (tid + u * threads < n) top(tid + u * threads, v[u]);
-  for (int c = tid + HELD * threads; c < n; c += threads) {
-    const int i = c / per, col = 8 * (c - i * per);
-    top(c, col < K ? *reinterpret_cast<const u32x4*>(row(i) + col) : none);
+  __device__ __forceinline__ int first() const { return 8 * (lane + 64 * (wv & (G - 1))); }
+  __device__ __forceinline__ u32x4 piece(int i, int c) const {
+    return c < K ? *reinterpret_cast<const u32x4*>(row(i) + c) : u32x4{0, 0, 0, 0};
   }
-  __syncthreads();
-  auto put = [&](int c, const u32x4& x) {
-    const int i = c / per, col = 8 * (c - i * per);
-    float f, s;
-    int8_factor(__uint_as_float(amax[i]), f, s);
-    *reinterpret_cast<uint2*>(codes + i * (Kp + 16) + col) = int8_codes8(x, f);
-    if (col == 0) scales[i] = s;
-  };
+  __device__ __forceinline__ void load() {
+    const int i = min(wv / G, rows - 1);
 #pragma unroll
-  for (int u = 0; u < HELD; ++u)
-    if (tid + u * threads < n) put(tid + u * threads, v[u]);
-  for (int c = tid + HELD * threads; c < n; c += threads) {
-    const int i = c / per, col = 8 * (c - i * per);
-    put(c, col < K ? *reinterpret_cast<const u32x4*>(row(i) + col) : none);
+    for (int u = 0; u < HELD; ++u) v[u] = piece(i, first() + u * 512 * G);
   }
-  __syncthreads();
-}
+  __device__ __forceinline__ void store(uint8_t* codes, float* scales, uint32_t* part) {
+    const int Kp = int8_pad(K), step = 512 * G;
+    for (int i = wv / G; i < rows || G > 1; i += KS / G) {  // G > 1: every wave once
+      const bool held = i == wv / G && i < rows;
+      uint32_t m = kFp8TinyBits;
+      if (held) {
+#pragma unroll
+        for (int u = 0; u < HELD; ++u) m = fp8_amax8(v[u], m);
+      }
+      for (int c = first() + (held ? HELD * step : 0); c < K && i < rows; c += step) m = fp8_amax8(piece(i, c), m);
+      // magnitudes on their bits, so that a NaN, above everything, stays
+      uint32_t b = max_lanes<64>(max(m << 16, m & 0xFFFF0000u));
+      if (G > 1) {
+        if (lane == 0) part[wv] = b;
+        __syncthreads();
+        for (int w = 0; w < G; ++w) b = max(b, part[(wv & -G) + w]);
+      }
+      if (i < rows) {
+        float f, s;
+        int8_factor(__uint_as_float(b), f, s);
+        uint8_t* to = codes + i * (Kp + 16);
+        if (held) {
+#pragma unroll
+          for (int u = 0; u < HELD; ++u)
+            if (first() + u * step < Kp) *reinterpret_cast<uint2*>(to + first() + u * step) = int8_codes8(v[u], f);
+        }
+        for (int c = first() + (held ? HELD * step : 0); c < Kp; c += step)
+          *reinterpret_cast<uint2*>(to + c) = int8_codes8(piece(i, c), f);
+        if (lane == 0 && (wv & (G - 1)) == 0) scales[i] = s;
+      }
+      if (G > 1) break;
+    }
+    __syncthreads();
+  }
+};
 
 template <int NT, int R, int KS, int D, Int8Mode MODE, bool BLOCK>
 __global__ __launch_bounds__(64 * KS) void int8_stream_kernel(Int8Args a) {
@@ -222,6 +231,12 @@ __global__ __launch_bounds__(64 * KS) void int8_stream_kernel(Int8Args a) {
         }
       }
     };
+    auto rows_of = [&](int i) { return a.x + (size_t)source(r0 + i) * a.ldx; };
+    BlockQuantizer<KS, BLOCK ? 4 : 1, decltype(rows_of)> quantizer(rend - r0, a.K, wv, lane, rows_of);
+    if constexpr (BLOCK) {
+      quantizer.load();
+      asm volatile("" ::: "memory");  // before the weights
+    }
     // this wave's steps wv, wv + KS, ...: D of them in flight
     const int n = wv < KB ? (KB - wv + KS - 1) / KS : 0;
     Step st[D];
@@ -230,9 +245,7 @@ __global__ __launch_bounds__(64 * KS) void int8_stream_kernel(Int8Args a) {
       for (int u = 0; u < D; ++u)
         if (u == 0 || u < n) load(st[u], wv + u * KS);
     }
-    if constexpr (BLOCK)  // while the first weights are on their way
-      quantize_block<4>(quantized, qscale, qmax, rend - r0, a.K, tid, 64 * KS,
-                        [&](int i) { return a.x + (size_t)source(r0 + i) * a.ldx; });
+    if constexpr (BLOCK) quantizer.store(quantized, qscale, qmax);  // while the first weights are on their way
     if (n > 0) {
       int i = 0;
       for (; i + 2 * D <= n; i += D) {
@@ -319,24 +332,33 @@ hipError_t launch_one(const Int8Args& a, int cus, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Items of 64 weight rows of a grouped product whose tiles hold `per` rows, at most.
+long long items64(Int8Mode mode, const Int8Args& a, int per) {
+  return most_tiles(a, per) * (mode == INT8_GATE_UP ? (a.N / 2 + 31) / 32 : (a.N + 63) / 64);
+}
+
 template <Int8Mode MODE>
 hipError_t launch_grouped(const Int8Args& a, int cus, hipStream_t s) {
-  if (a.cap > 0) {
-    const long long slabs = MODE == INT8_GATE_UP ? (a.N / 2 + 31) / 32 : (a.N + 63) / 64;  // of 64 rows
-    return most_tiles(a, a.cap) * slabs <= 3LL * cus / 2 ? launch_one<1, 2, 4, 4, MODE, true>(a, cus, s)
-                                                         : launch_one<1, 4, 4, 2, MODE, true>(a, cus, s);
-  }
+  // quantising: items of 32 weight rows and more steps in flight while there are few
+  if (a.cap > 0)
+    return items64(MODE, a, a.cap) <= 3LL * cus / 2 ? launch_one<1, 2, 4, 4, MODE, true>(a, cus, s)
+                                                    : launch_one<1, 4, 4, 3, MODE, true>(a, cus, s);
   return a.rows <= 16LL * a.E ? launch_one<1, 4, 4, 2, MODE, false>(a, cus, s) : launch_one<2, 4, 4, 2, MODE, false>(a, cus, s);
 }
 
 }  // namespace
 
+// Dense: quantising in every block of the product pays while it is little work (4 rows of 2816 x 4096 6.4 us, codes 5.7
+// behind a launch of 3.5; 8 rows 6.0 behind it).
 bool int8_decode_fits(int M, int K) { return M <= 16 && M * (int8_pad(K) / 128) <= 224; }
 
-// A tile holds an expert's rows of up to 16 tokens where two blocks' codes fit a CU's LDS.
-int int8_block_rows(int T, int K) {
+// Grouped: while every block has one item (3 blocks a compute unit), since a second item's rows are quantised with no
+// weights on their way beside it (H 7168, I 2048, 256 experts, top-8: gate / up of one token 46.6 us against 42.3 and the
+// quantiser's launch of 4.6, of two, in 1.3 rounds, 101 against 80.7; H 4096, I 1408, 64 experts, top-6, one token 20.4
+// against 21.7 and 3.8), and two blocks' codes fit a CU's LDS.  0: codes.
+int int8_block_rows(Int8Mode mode, const Int8Args& a, int T, int cus) {
   const int cap = min(T, 16);
-  return block_lds(cap, K) <= kBlockLds ? cap : 0;
+  return block_lds(cap, a.K) <= kBlockLds && items64(mode, a, cap) <= 3LL * cus ? cap : 0;
 }
 
 hipError_t launch_int8_stream(Int8Mode mode, const Int8Args& a, int cus, hipStream_t s) {

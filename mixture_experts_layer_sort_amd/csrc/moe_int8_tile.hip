@@ -381,20 +381,25 @@ hipError_t launch_tile(const Int8Args& a, long long token_tiles, int band, int c
 
 using Big = TileShape<4, 2, 4, 8, 2>;  // 256 weight rows x 256 tokens
 
-// Rounds of a dense product's tiles on `cus` compute units (one block each) times the time of a step.
+// Nanoseconds of a dense product: rounds of its tiles on `cus` compute units (one block each) x (first loads and
+// epilogue + K blocks x step).
 template <class S>
-long long dense_cost(const Int8Args& a, int cus, int ns_per_block) {
+long long dense_cost(const Int8Args& a, int cus, int fixed, int step) {
   const long long tiles = (long long)((a.rows + S::BT - 1) / S::BT) * ((a.N + S::BN - 1) / S::BN);
-  return (tiles + cus - 1) / cus * ns_per_block;
+  return (tiles + cus - 1) / cus * (fixed + (long long)(int8_pad(a.K) / 128) * step);
 }
 
+// Large tiles have the fewest operand bytes per product, small ones fill the GPU when there are few, and share K over
+// groups of waves.  The shape with the least cost is taken; its two numbers are fitted to 17 to 4096 rows of 576 x 7168,
+// 2816 x 4096, 4096 x 7168, 7168 x 2048, 18432 x 7168 and 1000 x 2000, where every choice is within a tenth of the best.
 hipError_t launch_dense(const Int8Args& a, int cus, hipStream_t s) {
   using T0 = TileShape<2, 1, 1, 4, 3, 4>;  // 32 x 64, K over 4 groups of waves
   using T1 = TileShape<4, 1, 1, 4, 4, 2>;  // 64 x 64, K over 2
   using T2 = TileShape<4, 1, 2, 4, 3, 2>;  // 128 x 64, K over 2
   using T3 = TileShape<4, 2, 2, 4, 4>;     // 128 x 128
-  const long long cost[5] = {dense_cost<T0>(a, cus, 168), dense_cost<T1>(a, cus, 246), dense_cost<T2>(a, cus, 366),
-                             dense_cost<T3>(a, cus, 500), dense_cost<Big>(a, cus, 980)};
+  const long long cost[5] = {dense_cost<T0>(a, cus, 3100, 158), dense_cost<T1>(a, cus, 3700, 190),
+                             dense_cost<T2>(a, cus, 4300, 270), dense_cost<T3>(a, cus, 8000, 300),
+                             dense_cost<Big>(a, cus, 12000, 950)};
   int best = 4;
   for (int i = 3; i >= 0; --i)
     if (cost[i] < cost[best]) best = i;
