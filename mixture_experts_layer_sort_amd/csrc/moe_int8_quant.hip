@@ -46,9 +46,7 @@ __global__ __launch_bounds__(256) void int8_quantize_weights_kernel(int K, const
 // Rows of x: a wave (WPR = 1, four rows per block) or a block (WPR = 4) per row, which stays in registers between its
 // maximum and its codes up to kHeld chunks of 8 values per lane; longer rows are read again.  Bound by memory: 2 bytes in,
 // 1 out per value.  The last block of a grouped launch writes the token tiles instead.
-constexpr int kHeld = 16;
-
-template <int WPR>
+template <int WPR, int kHeld>
 __global__ __launch_bounds__(256) void int8_quantize_rows_kernel(int M, int K, const uint16_t* x, long long ldx,
                                                                  int8_t* xq, float* xs, TileList list) {
   __shared__ float part[4];
@@ -90,11 +88,14 @@ __global__ __launch_bounds__(256) void int8_quantize_rows_kernel(int M, int K, c
 
 hipError_t launch_rows(int M, int K, const uint16_t* x, long long ldx, int8_t* xq, float* xs, const TileList& list,
                        hipStream_t s) {
-  const bool wave = M >= 1024 && K <= 64 * 8 * kHeld;
+  const bool wave = M >= 1024 && K <= 64 * 8 * 16;
   const long long blocks = (wave ? ((long long)M + 3) / 4 : M) + (list.tiles ? 1 : 0);
   if (blocks >= 1LL << 24) return hipErrorInvalidValue;
-  if (wave) int8_quantize_rows_kernel<1><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(M, K, x, ldx, xq, xs, list);
-  else int8_quantize_rows_kernel<4><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(M, K, x, ldx, xq, xs, list);
+  const dim3 grid((unsigned)blocks), block(256);
+  if (wave) int8_quantize_rows_kernel<1, 16><<<grid, block, 0, s>>>(M, K, x, ldx, xq, xs, list);
+  else if (K <= 256 * 8 * 2) int8_quantize_rows_kernel<4, 2><<<grid, block, 0, s>>>(M, K, x, ldx, xq, xs, list);
+  else if (K <= 256 * 8 * 4) int8_quantize_rows_kernel<4, 4><<<grid, block, 0, s>>>(M, K, x, ldx, xq, xs, list);
+  else int8_quantize_rows_kernel<4, 16><<<grid, block, 0, s>>>(M, K, x, ldx, xq, xs, list);
   return hipGetLastError();
 }
 
