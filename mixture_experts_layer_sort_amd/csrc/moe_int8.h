@@ -39,6 +39,8 @@ struct Int8Args {
   const int* pairs;     // sorted pairs; unused by DENSE
   const int4* tiles;    // tiled kernel: token tiles
   const int* ntiles;
+  int* sums;            // tiled kernel, DENSE with splits > 1: [splits][rows][int8_sums_ld(N)]
+  int splits;           // runs of K blocks, of different blocks of the launch (0, 1: one)
   uint16_t* out;        // bf16 rows, ldo apart (GATE_UP: the intermediate)
   long long ldo;
   int rows, E, N, K, k;
@@ -100,6 +102,10 @@ int int8_block_rows(Int8Mode mode, const Int8Args& a, int T, int cus);  // Int8A
 hipError_t launch_int8_stream(Int8Mode mode, const Int8Args& a, int cus, hipStream_t s);
 // The tiled kernel (reads codes).  Grouped modes: `tile` sorted rows per token tile, token_tiles: at least their number.
 hipError_t launch_int8_tile(Int8Mode mode, const Int8Args& a, int tile, long long token_tiles, int cus, hipStream_t s);
+// Dense products of few tiles and a long K: K in this many runs (> 1), whose sums a second launch adds; 1: not this way.
+int int8_splits(int M, int N, int K);
+size_t int8_split_bytes(int max_M, int N, int K);  // of the sums for any M <= max_M
+__host__ __device__ inline int int8_sums_ld(int N) { return (N + 3) / 4 * 4; }
 int int8_tile_tokens(long long rows, int experts);  // sorted rows per tile of the grouped modes
 constexpr int kInt8TileTokensMin = 64;
 constexpr int kInt8TileGroup = 4;  // tiles of an expert that share a weight slab next to each other

@@ -38,13 +38,14 @@ bool int8_shape_ok(int32_t N, int32_t K) {
 }
 
 struct LinearWorkspace {
-  size_t xq, xs, total;
+  size_t xq, xs, sums, total;
 };
-LinearWorkspace linear_workspace(size_t M, int K) {
+LinearWorkspace linear_workspace(size_t M, int N, int K) {
   LinearWorkspace w;
   w.xq = 0;
   w.xs = up256(M * int8_pad(K));
-  w.total = w.xs + up256(M * sizeof(float));
+  w.sums = w.xs + up256(M * sizeof(float));
+  w.total = w.sums + up256(int8_split_bytes((int)M, N, K));
   return w;
 }
 
@@ -95,7 +96,7 @@ moe_status moe_int8_quantize_weights(int32_t count, int32_t rows, int32_t K, con
 
 size_t moe_int8_linear_workspace_bytes(int32_t max_M, int32_t N, int32_t K) {
   if (max_M < 1 || max_M > (1 << 24) || !int8_shape_ok(N, K)) return 0;
-  return linear_workspace(max_M, K).total;
+  return linear_workspace(max_M, N, K).total;
 }
 
 moe_status moe_int8_linear(int32_t M, int32_t N, int32_t K, const void* codes, const float* scales, const uint16_t* x,
@@ -109,7 +110,7 @@ moe_status moe_int8_linear(int32_t M, int32_t N, int32_t K, const void* codes, c
     return MOE_ERR_INVALID_ARG;
   if (x_stride < K || x_stride % 8 || out_stride < N) return MOE_ERR_INVALID_ARG;
   if (x_stride > (1LL << 32) || out_stride > (1LL << 32)) return MOE_ERR_UNSUPPORTED;
-  const LinearWorkspace W = linear_workspace(M, K);
+  const LinearWorkspace W = linear_workspace(M, N, K);
   if (ws_bytes < W.total) return MOE_ERR_WORKSPACE;
   Int8Args a = {};
   a.w = (const int8_t*)codes;
@@ -125,6 +126,8 @@ moe_status moe_int8_linear(int32_t M, int32_t N, int32_t K, const void* codes, c
   }
   int8_t* xq = (int8_t*)ws + W.xq;
   float* xs = (float*)((uint8_t*)ws + W.xs);
+  a.splits = int8_splits(M, N, K);
+  a.sums = (int*)((uint8_t*)ws + W.sums);
   const hipError_t e = launch_int8_quantize_rows(M, K, x, x_stride, xq, xs, stream);
   if (e != hipSuccess) return MOE_ERR_LAUNCH;
   a.xq = xq;
@@ -132,7 +135,7 @@ moe_status moe_int8_linear(int32_t M, int32_t N, int32_t K, const void* codes, c
   a.xrows = M;
   // 17 to 32 rows: the streaming kernel while it is one round of blocks of 16 weight rows (17 rows of 2816 x 4096 10.1 us,
   // tiled 11.4; of 7168 x 2048 11.1 and 9.4; of 18432 x 7168 46 and 26)
-  if (M <= 16 || (M <= 32 && N <= 16 * cu_count())) return launched(launch_int8_stream(INT8_DENSE, a, cu_count(), stream));
+  if (a.splits <= 1 && (M <= 16 || (M <= 32 && N <= 16 * cu_count()))) return launched(launch_int8_stream(INT8_DENSE, a, cu_count(), stream));
   return launched(launch_int8_tile(INT8_DENSE, a, 0, 0, cu_count(), stream));
 }
 

@@ -75,15 +75,16 @@ constexpr bool takes_turns() {
 }
 
 // One tile: weight rows from n0 on (GATE_UP: gate rows, and their up rows) by up to BT token rows from r0 on, of expert e's
-// that end at rend.
-template <class S, Int8Mode MODE>
-__device__ __forceinline__ void run_tile(const Int8Args& a, uint8_t* shared, int e, int r0, int rend, int n0) {
+// that end at rend.  SPLIT: K blocks [kb0, kb1) of them, whose sums are stored.
+template <class S, Int8Mode MODE, bool SPLIT = false>
+__device__ __forceinline__ void run_tile(const Int8Args& a, uint8_t* shared, int e, int r0, int rend, int n0, int kb0 = 0,
+                                         int kb1 = 0) {
   const int tid = threadIdx.x, lane = tid & 63, gw = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int kg = S::KG > 1 ? gw / S::NW : 0, wv = S::KG > 1 ? gw % S::NW : gw;  // K group, wave in it
   const int r = lane & 15, q = lane >> 4;
   const int wr = wv % S::WR, wt = wv / S::WR;
-  const int Kp = int8_pad(a.K), KB = Kp / 128;
-  const int steps = (KB + S::KG - 1) / S::KG;  // step s of group g: K block s KG + g
+  const int Kp = int8_pad(a.K), KB = SPLIT ? kb1 : Kp / 128;
+  const int steps = ((SPLIT ? kb1 - kb0 : KB) + S::KG - 1) / S::KG;  // step s of group g: K block kb0 + s KG + g
   const int nspan = MODE == INT8_GATE_UP ? a.N / 2 : a.N;          // output columns
   constexpr int kSpan = MODE == INT8_GATE_UP ? S::BN / 2 : S::BN;  // per tile
   uint8_t* lds = shared + kg * S::kRing;
@@ -121,7 +122,7 @@ __device__ __forceinline__ void run_tile(const Int8Args& a, uint8_t* shared, int
   // The loads of one step, one by one (X: LA of weights, LB / 2 of tokens; Y: LB / 2).  Steps past the last one load the
   // last one again (into a stage that is not read any more), so that the counts of the waits hold to the end.
   auto stage = [&](int step) { return lds + (S::kTwo ? step & 1 : step % S::NS) * S::kStage; };
-  auto k_of = [&](int step) { return min(step * S::KG + kg, KB - 1) * 128; };
+  auto k_of = [&](int step) { return min((SPLIT ? kb0 : 0) + step * S::KG + kg, KB - 1) * 128; };
   auto load_tokens = [&](int step, int j) {
     const int k = k_of(step);
     load_lds16(rsrc_of(xbase + k, xbytes - k), xoff[j], stage(step) + S::kA + tok_row(j) * 128);
@@ -184,7 +185,7 @@ __device__ __forceinline__ void run_tile(const Int8Args& a, uint8_t* shared, int
 #pragma unroll 1
     for (int step = 0; step < steps; ++step) {
       const uint8_t *st = stage(step), *sn = stage(step + 1);
-      if (S::KG > 1 && step * S::KG + kg >= KB) {  // a group that has run out: its weights count as zero
+      if (S::KG > 1 && (SPLIT ? kb0 : 0) + step * S::KG + kg >= KB) {  // a group that has run out: its weights count as zero
 #pragma unroll
         for (int f = 0; f < S::RF; ++f) A[f].lo = A[f].hi = u32x4{0, 0, 0, 0};
       }
@@ -267,6 +268,22 @@ __device__ __forceinline__ void run_tile(const Int8Args& a, uint8_t* shared, int
     wait_barrier<0>();
   }
   lds = shared;
+  if constexpr (SPLIT) {  // this run's sums, as they lie: a lane's four weight rows are neighbours
+    static_assert(MODE == INT8_DENSE, "runs of dense tiles");
+    if (kg > 0) return;
+    const int ld = int8_sums_ld(a.N);
+    int* sums = a.sums + (size_t)blockIdx.y * a.rows * ld;
+#pragma unroll
+    for (int t = 0; t < S::TF; ++t) {
+      const int row = r0 + 16 * (t * S::WT + wt) + r;
+#pragma unroll
+      for (int f = 0; f < S::RF; ++f) {
+        const int n = n0 + frag_row(f) + 4 * q;
+        if (row < rend && n < ld) *reinterpret_cast<i32x4*>(sums + (size_t)row * ld + n) = acc[f][t];
+      }
+    }
+    return;
+  }
 
   // accumulator (f, t) element i of lane r + 16 q: tile row frag_row(f) + 4 q + i, token 16 (t WT + wt) + r.  Through
   // LDS, so that whole rows are stored: rows of kSpan values, 16-byte pieces at c ^ (token % pieces).
@@ -388,6 +405,41 @@ hipError_t launch_tile(const Int8Args& a, long long token_tiles, int band, int c
   return hipGetLastError();
 }
 
+// Dense products of few tiles and a long K: blockIdx.y is a run of K blocks; a second launch joins the runs.
+template <class S>
+__global__ __launch_bounds__(64 * S::NW * S::KG) void int8_split_kernel(Int8Args a) {
+  extern __shared__ __align__(256) uint8_t shared[];
+  const int NB = (a.N + S::BN - 1) / S::BN, KB = int8_pad(a.K) / 128, run = (KB + a.splits - 1) / a.splits;
+  const int tile = blockIdx.x, kb0 = blockIdx.y * run;
+  run_tile<S, INT8_DENSE, true>(a, shared, 0, tile / NB * S::BT, a.rows, tile % NB * S::BN, kb0, min(KB, kb0 + run));
+}
+
+__global__ __launch_bounds__(256) void int8_join_kernel(Int8Args a) {  // a thread per four columns
+  const int ld = int8_sums_ld(a.N), c = blockIdx.x * 256 + threadIdx.x, row = c / (ld / 4), n = 4 * (c - row * (ld / 4));
+  if (row >= a.rows) return;
+  const i32x4* p = reinterpret_cast<const i32x4*>(a.sums) + c;
+  i32x4 v = p[0];
+#pragma unroll 8
+  for (int i = 1; i < a.splits; ++i) v += p[(size_t)i * a.rows * (ld / 4)];
+  const float sx = a.xs[row];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < a.N) a.out[(size_t)row * a.ldo + n + i] = f32_to_bf16(value(v[i], sx, a.wsc[n + i]));
+}
+
+using Split = TileShape<2, 1, 1, 4, 3, 4>;  // 32 x 64, K over 4 groups of waves
+
+hipError_t launch_split(const Int8Args& a, hipStream_t s) {
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&int8_split_kernel<Split>),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, Split::kLds);
+  if (e != hipSuccess) return e;
+  const int tiles = ((a.rows + Split::BT - 1) / Split::BT) * ((a.N + Split::BN - 1) / Split::BN);
+  int8_split_kernel<Split><<<dim3(tiles, a.splits), dim3(64 * Split::NW * Split::KG), Split::kLds, s>>>(a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  int8_join_kernel<<<dim3((a.rows * (int8_sums_ld(a.N) / 4) + 255) / 256), dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+
 // Nanoseconds of a dense product: rounds of its tiles on `cus` compute units (one block each) x (first loads and
 // epilogue + K blocks x step).
 template <class S>
@@ -400,7 +452,8 @@ long long dense_cost(const Int8Args& a, int cus, int fixed, int step) {
 // groups of waves.  The shape with the least cost is taken; its two numbers are fitted to 17 to 4096 rows of 576 x 7168,
 // 2816 x 4096, 4096 x 7168, 7168 x 2048, 18432 x 7168 and 1000 x 2000, where every choice is within a tenth of the best.
 hipError_t launch_dense(const Int8Args& a, int cus, hipStream_t s) {
-  using T0 = TileShape<2, 1, 1, 4, 3, 4>;  // 32 x 64, K over 4 groups of waves
+  if (a.splits > 1) return launch_split(a, s);
+  using T0 = Split;                        // 32 x 64, K over 4 groups of waves
   using T1 = TileShape<4, 1, 1, 4, 4, 2>;  // 64 x 64, K over 2
   using T2 = TileShape<4, 1, 2, 4, 3, 2>;  // 128 x 64, K over 2
   using T3 = TileShape<4, 2, 2, 4, 4>;     // 128 x 128
@@ -427,6 +480,31 @@ hipError_t launch_grouped(const Int8Args& a, int tile, long long token_tiles, in
 }
 
 }  // namespace
+
+// Runs of at least 8 blocks of 128 (two steps of the kernel's four groups), as many as fill 256 compute units, where that
+// saves more steps (158 ns each) than the second launch costs (quantiser, runs and join, us, against quantiser and one
+// launch: 33 rows of 576 x 7168 12.3 and 15.0, of 200 x 7008 12.6 and 14.9; 16 rows 12.3 and 12.1; in two runs 64 rows of
+// 4096 x 7168 16.5 and 15.5).  Joining by atomic additions in one launch took 18 us for its runs alone.
+constexpr int kSplitRows = 128, kSplitRun = 8, kSplitBlocks = 256, kSplitSaves = 22;
+
+int int8_splits(int M, int N, int K) {
+  const int KB = int8_pad(K) / 128;
+  if (M <= 16 || M > kSplitRows || N > kSplitBlocks / 2 * Split::BN) return 1;
+  const int tiles = (M + Split::BT - 1) / Split::BT * ((N + Split::BN - 1) / Split::BN);
+  const int n = min(KB / kSplitRun, kSplitBlocks / tiles);
+  if (n < 3) return 1;
+  const int run = (KB + n - 1) / n;
+  return KB - run >= kSplitSaves ? (KB + run - 1) / run : 1;  // no empty run
+}
+
+size_t int8_split_bytes(int max_M, int N, int K) {
+  size_t n = 0;
+  for (int M = Split::BT; M < max_M + Split::BT && M <= kSplitRows; M += Split::BT) {  // fewer rows of as many tiles need less
+    const int rows = min(M, max_M), splits = int8_splits(rows, N, K);
+    if (splits > 1) n = max(n, (size_t)splits * rows * int8_sums_ld(N) * sizeof(int));
+  }
+  return n;
+}
 
 int int8_tile_tokens(long long rows, int experts) {
   return rows < 48 * experts ? Few::BT : rows < 160 * experts ? Mid::BT : Big::BT;

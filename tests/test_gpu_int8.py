@@ -53,7 +53,8 @@ def _linear(x, c, s, stride=None, ostride=None, fill=7.0):
 SIZES = [(1, 1, 16), (1, 7, 48), (2, 130, 272), (5, 64, 128), (8, 200, 2048), (1, 2816, 4096), (16, 96, 7168),
          (17, 576, 2304), (31, 50, 144), (32, 257, 1040), (33, 64, 512), (64, 320, 4096), (65, 1000, 272), (100, 513, 640),
          (129, 128, 1152), (200, 300, 4112), (256, 256, 256), (300, 2000, 2000), (511, 1408, 768), (1030, 700, 1296),
-         (2100, 257, 144), (700, 4100, 2064)]
+         (2100, 257, 144), (700, 4100, 2064),
+         (17, 576, 7168), (70, 203, 6000), (128, 301, 4096)]  # the last three: K in runs
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
