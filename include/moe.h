@@ -493,7 +493,8 @@ MOE_API moe_status moe_int8_quantize_weights(int32_t count, int32_t rows, int32_
  * 2^17; both strides at most 2^32 (else MOE_ERR_UNSUPPORTED); M <= 2^24, 0 is a
  * no-op.  codes and x must be aligned to 16 bytes, scales to 4, ws to 256.
  * Workspace: moe_int8_linear_workspace_bytes(max_M, N, K) bytes serve any M <=
- * max_M (0 for unsupported arguments); its contents need not survive a call. */
+ * max_M (0 for unsupported arguments); its contents need not survive a call, and
+ * calls that share it must be stream-ordered. */
 MOE_API size_t moe_int8_linear_workspace_bytes(int32_t max_M, int32_t N, int32_t K);
 MOE_API moe_status moe_int8_linear(int32_t M, int32_t N, int32_t K, const void* codes, const float* scales,
                                    const uint16_t* x, int64_t x_stride, uint16_t* out, int64_t out_stride, void* ws,
@@ -512,7 +513,8 @@ MOE_API moe_status moe_int8_linear(int32_t M, int32_t N, int32_t K, const void* 
  * MOE_SWIGLU, hidden and inter at most 2^17, else MOE_ERR_UNSUPPORTED.  codes, x
  * and y must be aligned to 16 bytes, scales, offsets and pairs to 4, ws
  * (moe_int8_experts_workspace_bytes(shape) bytes, 0 for an unsupported shape) to
- * 256.  T == 0 is a no-op. */
+ * 256; calls that share it must be stream-ordered.  Outputs must not overlap
+ * inputs.  T == 0 is a no-op. */
 MOE_API size_t moe_int8_experts_workspace_bytes(const moe_shape* shape);
 MOE_API moe_status moe_int8_experts(const moe_shape* shape, int32_t T, const void* w13_codes, const float* w13_scales,
                                     const void* w2_codes, const float* w2_scales, const int32_t* offsets,
@@ -533,7 +535,7 @@ MOE_API moe_status moe_int8_experts(const moe_shape* shape, int32_t T, const voi
  * itself with no residual.  out may be the residual; else outputs must not overlap
  * inputs.  8 <= H <= 16384, H % 8 == 0, 0 <= k <= 32, T and T k at most 2^24 (else
  * MOE_ERR_UNSUPPORTED); eps >= 0 and scale finite.  bf16 arrays must be aligned
- * to 16 bytes, fp32 ones to 4. */
+ * to 16 bytes, fp32 ones to 4.  A row of zeros with eps = 0 is 0 / 0, NaN. */
 MOE_API moe_status moe_combine_norm(int32_t T, int32_t H, int32_t k, const uint16_t* y, const float* topk_w,
                                     const uint16_t* shared, const float* shared_gate, const uint16_t* residual,
                                     const uint16_t* post_weight, const uint16_t* next_weight, float eps, float scale,
@@ -546,7 +548,7 @@ MOE_API moe_status moe_combine_norm(int32_t T, int32_t H, int32_t k, const uint1
  *   moe_route_scores_backward and moe_route_backward take), d_shared bf16 [T, H],
  *   d_gate fp32 [T]: each NULL if it is not wanted;
  *   d_post_weight, d_next_weight fp32 [H]: given with their weights; sums over the
- *   tokens in an order that depends on T alone.
+ *   tokens in an order that depends on T and H alone.
  * d_residual may be d_out; else outputs must not overlap inputs.  Workspace (with
  * post_weight or next_weight): moe_combine_norm_backward_workspace_bytes(max_T, H)
  * bytes serve any T <= max_T (0 for unsupported arguments), aligned to 256; need

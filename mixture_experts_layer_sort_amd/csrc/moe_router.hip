@@ -428,7 +428,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
   wave_lds_sync();
   if (id >= 0) atomicAdd(&mine[id], (float)part);
   wave_lds_sync();
-  if (t >= a.T) return;
+  if (t >= a.T || (a.accumulate && !keep)) return;  // a masked row stays as it is
   float* out = a.d_logits + t * a.ldd;
 #pragma unroll
   for (int i = 0; i < N; i += 4) {

@@ -206,6 +206,17 @@ def test_gradient_of_odd_picks(kind, renorm, T):
     _close(_grad(z, ids, dw, kind, renorm, 1.0, mask), ref, mag)
 
 
+@pytest.mark.parametrize("T,stride", [(50, 64), (2100, 64), (50, 65)])
+def test_masked_rows_stay_as_they_are(T, stride):
+    """Adding to what is there leaves a masked row's bits alone: negative zeros and NaN too."""
+    rng, z, ids, dw = _case(T, 64, 4, 13)
+    mask = (np.arange(T) % 3 == 0).astype(np.uint8)
+    start = np.full((T, 64), -0.0, np.float32)
+    start[:, ::5], start[:, 1::5] = np.nan, -np.inf
+    g = _grad(z, ids, dw, "softmax", False, 1.0, mask, start, dstride=stride)
+    assert np.array_equal(g[mask == 0].view(np.uint32), start[mask == 0].view(np.uint32))
+
+
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 def test_gradient_of_switched_off_experts(kind):
     rng, z, ids, dw = _case(40, 32, 4, 10)
