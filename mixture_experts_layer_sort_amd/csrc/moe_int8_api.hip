@@ -72,6 +72,16 @@ ExpertsWorkspace experts_workspace(const moe_shape* s) {
   return w;
 }
 
+// Experts by the streaming kernel: up to 8 rows an expert while the tiles (128 intermediate columns of an expert that has
+// rows) are fewer than 12 rounds of the GPU, and up to 32 rows while they are a quarter of one round.  Us, streaming / tiled:
+// 256 experts of 7168 x 2048, top-8, 16 tokens 734 / 765, 24 893 / 922, 96 1744 / 1706; 64 of 4096 x 1408, top-6, 8 tokens
+// 130 / 150, 24 184 / 215, 64 221 / 229, 128 243 / 231; 8 of 4096 x 7168, top-2, 32 tokens 137 / 160, 64 174 / 161; 2 of 4096
+// x 1024, 64 tokens 28 / 40.
+bool int8_streams(int P, int E, int I, int cus) {
+  const long long columns = I / 128;
+  return (P <= 8LL * E && (P < E ? P : E) * columns < 12LL * cus) || (P <= 32LL * E && E * columns <= cus / 4);
+}
+
 moe_status check_experts(const moe_shape* s) {
   const moe_status st = moe_check_shape(s);
   if (st != MOE_OK) return st;
@@ -192,9 +202,7 @@ moe_status moe_int8_experts(const moe_shape* s, int32_t T, const void* w13_codes
   down.ldo = H;
   down.N = H, down.K = I;
 
-  // The tiled kernel; the streaming one for up to 8 tokens of 48 rows, where the tiles (128 intermediate columns each)
-  // would leave half of the compute units idle, and for gathered rows beyond the tiled kernel's 32-bit addresses.
-  if ((T > 8 || P > 48) && (long long)P * (I / 128) > cus / 2 && (long long)T * H < (1LL << 31)) {
+  if (!int8_streams(P, s->num_experts, I, cus) && (long long)T * H < (1LL << 31)) {  // 32-bit offsets of gathered rows
     const int tile = int8_tile_tokens(P, s->num_experts);
     const long long ntok = (long long)max_tiles(s, P, tile);
     if (launch_int8_quantize_tokens(T, H, x, xq, xs, offsets, s->num_experts, tile, (int4*)(base + W.tiles),

@@ -355,10 +355,13 @@ bool int8_decode_fits(int M, int K) { return M <= 16 && M * (int8_pad(K) / 128) 
 // Grouped: while every block has one item (3 blocks a compute unit), since a second item's rows are quantised with no
 // weights on their way beside it (H 7168, I 2048, 256 experts, top-8: gate / up of one token 46.6 us against 42.3 and the
 // quantiser's launch of 4.6, of two, in 1.3 rounds, 101 against 80.7; H 4096, I 1408, 64 experts, top-6, one token 20.4
-// against 21.7 and 3.8), and two blocks' codes fit a CU's LDS.  0: codes.
+// against 21.7 and 3.8); while an expert's rows are little work (gate / up of H 4096 and 2 experts of I 1024, 8 tokens 13.5
+// against 12.6 and 2.7, 14 tokens 20.4 against 12.6 and 3.0; one of I 4096, 9 tokens 23.8 against 12.6 and 8.0); and while
+// two blocks' codes fit a CU's LDS.  0: codes.
 int int8_block_rows(Int8Mode mode, const Int8Args& a, int T, int cus) {
-  const int cap = min(T, 16);
-  return block_lds(cap, a.K) <= kBlockLds && items64(mode, a, cap) <= 3LL * cus ? cap : 0;
+  const int cap = min(T, 16), rows = min(cap, a.rows / a.E + 1);
+  const bool little = rows * (int8_pad(a.K) / 128) < 200;
+  return little && block_lds(cap, a.K) <= kBlockLds && items64(mode, a, cap) <= 3LL * cus ? cap : 0;
 }
 
 hipError_t launch_int8_stream(Int8Mode mode, const Int8Args& a, int cus, hipStream_t s) {

@@ -188,7 +188,8 @@ CASES = [  # T, H, I, E, k, skew, limit: the streaming kernel's sources, the til
     (8, 2048, 256, 12, 6, 0.0, 0.0), (9, 512, 128, 64, 8, 3.0, 0.0), (40, 4096, 128, 4, 2, 0.0, 1.0),
     (30, 256, 128, 2, 1, 0.0, 0.0), (64, 512, 768, 60, 4, 1.0, 0.0), (333, 512, 384, 16, 3, 0.5, 0.0),
     (500, 256, 256, 7, 2, 2.0, 3.0), (700, 384, 512, 6, 2, 1.0, 0.0), (1, 16640, 128, 4, 2, 0.0, 0.0),
-    (6, 256, 16640, 4, 2, 0.0, 0.0),
+    (6, 256, 16640, 4, 2, 0.0, 0.0), (120, 512, 768, 40, 4, 0.5, 0.0), (90, 256, 256, 6, 2, 1.0, 0.0),
+    (14, 4096, 128, 2, 1, 0.0, 0.0), (250, 384, 1408, 24, 4, 0.5, 1.0),
 ]
 
 
@@ -296,7 +297,7 @@ def test_rows_far_apart():
         assert np.array_equal(_bits(out[at, :N]), ref)
 
 
-@pytest.mark.parametrize("T", [2, 60])
+@pytest.mark.parametrize("T", [2, 60, 1100])
 def test_experts_weights_past_2_31(T):
     """260 experts of 2^23 + 2^22 codes: 3 2^30 of them; the last ones' rows."""
     d, H, I, E, k = gh.dev(), 4096, 1024, 260, 2
@@ -321,3 +322,31 @@ def test_experts_weights_past_2_31(T):
     pick = torch.from_numpy(used).to(d)
     a13, a2 = w13[pick].cpu().numpy(), w2[pick].cpu().numpy()
     _check_experts(_bits(y), int8.experts(x, a13, s13[used], a2, s2[used], off5, pairs, k), a2, s2[used], off5, pairs)
+
+
+def test_experts_of_more_than_2_31_values():
+    """16400 tokens of 131072 values: a token's rows are the same bits as in a batch of 300 (whose rows other kernels read
+    by 32-bit offsets)."""
+    d, H, I, E, k, T, n = gh.dev(), 1 << 17, 128, 3, 1, 16400, 300
+    g = torch.Generator(device=d).manual_seed(6)
+    w13 = torch.randint(-127, 128, (E, 2 * I, H), generator=g, device=d, dtype=torch.int8)
+    w2 = torch.randint(-127, 128, (E, H, I), generator=g, device=d, dtype=torch.int8)
+    s13 = torch.rand(E, 2 * I, generator=g, device=d) * 1e-5
+    s2 = torch.rand(E, H, generator=g, device=d) * 1e-3
+    x = torch.empty(T, H, dtype=torch.bfloat16, device=d).normal_(generator=g)
+    flat = torch.randint(0, E, (T,), generator=g, device=d)
+
+    def run(x, flat):
+        T = len(flat)
+        shape = lib.make_shape(H, I, E, k, T, "bf16")
+        off = torch.zeros(E + 1, dtype=torch.int32, device=d)
+        off[1:] = torch.bincount(flat, minlength=E).cumsum(0)
+        ws = torch.empty(lib.moe_int8_experts_workspace_bytes(shape), dtype=torch.uint8, device=d)
+        y = torch.full((T, H), 7.0, dtype=torch.bfloat16, device=d)
+        lib.moe_int8_experts(shape, T, w13, s13, w2, s2, off, flat.argsort(stable=True).int(), x, y, ws)
+        return y
+
+    y = run(x, flat)
+    for at in (slice(0, n), slice(T - n, T)):
+        assert torch.equal(y[at].view(torch.int16), run(x[at].contiguous(), flat[at]).view(torch.int16))
+        assert (y[at] != 7.0).any(dim=1).all()

@@ -206,3 +206,22 @@ def test_norm_gradient_workspace():
     assert sizes == sorted(sizes) and sizes[0] > 0
     for H in (8, 16, 504, 512, 520, 1024, 2048, 8192, 8200, 16384):  # both norms' parts of every block
         assert f(1, H) >= 8 * H and f(1 << 20, H) >= 256 * 8 * H, H
+
+
+def test_tiled_products_use_no_scratch():
+    """The tiled products count their loads in flight, which hold no operation that the compiler adds: none of those
+    kernels may keep registers in memory."""
+    import struct
+
+    msgpack = pytest.importorskip("msgpack")
+    with open(lib.LIB_PATH, "rb") as f:
+        data = f.read()
+    at, kernels = 0, {}
+    while (at := data.find(b"AMDGPU\0", at)) >= 0:
+        name, size, kind = struct.unpack("<III", data[at - 12:at])
+        if name == 7 and kind == 32:  # a code object's note of its kernels
+            for k in msgpack.unpackb(data[at + 8:at + 8 + size])["amdhsa.kernels"]:
+                kernels[k[".name"]] = k[".private_segment_fixed_size"]
+        at += 7
+    tiled = {n: v for n, v in kernels.items() if "int8_tile" in n or "int8_split" in n}
+    assert len(tiled) >= 12 and not any(tiled.values()), tiled
