@@ -7,6 +7,10 @@
 // 16 q + 16) and [64 + 16 q, + 16) of the step; which 32 of the 128 bytes a lane
 // holds does not matter, since tokens use the same order), D steps ahead.  The
 // waves' integer sums meet in LDS.
+//
+// Bound by reading the weights: one token of 8 of 256 experts of 7168 x 2048, gate / up
+// 46.6 us (235 MB, 5.0 TB/s), down 24.7 (117 MB, 4.8) behind 4.8 for the intermediate's
+// codes; 24 tokens 592 and 307.
 #include "moe_int8.h"
 #include "moe_wave.h"
 

@@ -1,5 +1,5 @@
 // Tiled product on 8-bit integer weights: many token rows per weight matrix
-// (prompts), bound by the matrix unit.
+// (prompts).
 //
 // Block tile = BN = 16 RF WR weight rows x BT = 16 TF WT tokens, by WR x WT
 // waves of RF x TF fragments each; step = 128 of K, two 16 x 16 x 64 matrix
@@ -24,6 +24,21 @@
 //
 // K that ends inside a step: the tokens' codes are zero from there on, and whatever
 // integers the weights' pieces hold, their products are.
+//
+// Bound by operand movement (LDS reads of both operands once per fragment, direct
+// loads) and, on long runs, by power: 8192 rows of 4096 x 7168 take 167 us on a cool
+// GPU and 196 at the median (2.9 and 2.5 PFLOP/s; matrix instructions alone reach 3.3 to
+// 3.9 on random bits, a library's 8-bit product 2.0 at this shape), 148 with zeros for
+// operands; without the matrix instructions the rest took 128 us of 133.  256 experts of
+// 7168 x 2048 with 8192 tokens, top-8: gate / up 2160 us, down 1300 (1.7 PFLOP/s: an
+// expert's tiles of 256 rows are two thirds full).  33 rows of 2816 x 4096: 8.6 us, of
+// which the weights' 12 MB are 2.4.
+//
+// At 8192 rows, us, against 176 of that time: four waves of 128 x 128 with accumulators
+// among the accumulation registers 212 (copies), fragments read in pairs 185 to 192,
+// waves that load apart from waves that compute on three weight stages the same, weights
+// stored tile by tile the same.  Weight fragments in two sets of registers spill, and a
+// spill's memory operations break the counts of the waits below.
 #include "moe_int8.h"
 
 namespace moe {

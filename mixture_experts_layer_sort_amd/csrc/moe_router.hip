@@ -19,6 +19,11 @@
 // in the keys as they were (picks of one lane with one value follow each other, the
 // n-th is the n-th such expert).  L = 16 (four tokens per wave share every exchange)
 // where there are tokens enough to fill the GPU, L = 64 for few tokens or many experts.
+//
+// Bound by arithmetic: 16384 x 256, sigmoid, 8 groups, top-8: 12.2 us, of which the 64-bit
+// scores are 4, the rounds 1.3, the sort 0.6 and the bytes (17.8 MB) 3.5; one token 3.7.
+// Gradient, bound by memory: 32768 x 256, sigmoid 9.7 us (34 MB written), softmax that is
+// not renormalised 13.4 (67 MB, 5.0 TB/s).
 #include "moe_router.h"
 
 #include "moe_wave.h"
