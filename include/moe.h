@@ -491,7 +491,8 @@ MOE_API moe_status moe_int8_quantize_weights(int32_t count, int32_t rows, int32_
  * bf16 [M, N] with rows out_stride elements apart (>= N); columns past N of an
  * out row are left as they are.  Any 1 <= N <= 2^20; K a multiple of 16, at most
  * 2^17; both strides at most 2^32 (else MOE_ERR_UNSUPPORTED); M <= 2^24, 0 is a
- * no-op.  codes and x must be aligned to 16 bytes, scales to 4, ws to 256.
+ * no-op.  codes and x must be aligned to 16 bytes, scales to 4, ws to 256; out
+ * must not overlap the inputs.
  * Workspace: moe_int8_linear_workspace_bytes(max_M, N, K) bytes serve any M <=
  * max_M (0 for unsupported arguments); its contents need not survive a call, and
  * calls that share it must be stream-ordered. */
