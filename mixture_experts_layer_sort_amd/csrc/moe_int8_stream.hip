@@ -23,14 +23,14 @@ __device__ __forceinline__ float value(int acc, float sx, float sw) { return (fl
 // Columns n .. n + 3 of an output row that ends at N.
 __device__ __forceinline__ void store4(uint16_t* row, int n, int N, const f32x4& v) {
   uint16_t* o = row + n;
-  const uint32_t b0 = f32_to_bf16(v[0]), b1 = f32_to_bf16(v[1]), b2 = f32_to_bf16(v[2]), b3 = f32_to_bf16(v[3]);
+  const uint32_t lo = bf16_pair(v[0], v[1]), hi = bf16_pair(v[2], v[3]);
   if (n + 4 <= N && ((uintptr_t)o & 7) == 0) {
-    *reinterpret_cast<uint2*>(o) = make_uint2(b0 | b1 << 16, b2 | b3 << 16);
+    *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
   } else {
-    if (n < N) o[0] = (uint16_t)b0;
-    if (n + 1 < N) o[1] = (uint16_t)b1;
-    if (n + 2 < N) o[2] = (uint16_t)b2;
-    if (n + 3 < N) o[3] = (uint16_t)b3;
+    if (n < N) o[0] = (uint16_t)lo;
+    if (n + 1 < N) o[1] = (uint16_t)(lo >> 16);
+    if (n + 2 < N) o[2] = (uint16_t)hi;
+    if (n + 3 < N) o[3] = (uint16_t)(hi >> 16);
   }
 }
 

@@ -40,6 +40,7 @@
 // stored tile by tile the same.  Weight fragments in two sets of registers spill, and a
 // spill's memory operations break the counts of the waits below.
 #include "moe_int8.h"
+#include "moe_wave.h"
 
 namespace moe {
 namespace {
@@ -330,8 +331,7 @@ __device__ __forceinline__ void run_tile(const Int8Args& a, uint8_t* shared, int
             v[i] = swiglu(v[i], value(acc[f + S::RF / 2][t][i], sx, sw[f + S::RF / 2][i]), a.limit);
         }
         *reinterpret_cast<uint2*>(lds + tok * (kSpan * 2) + (((col >> 3) ^ (tok & (kPieces - 1))) << 4) + (col & 4) * 2) =
-            make_uint2(f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
-                       f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16);
+            make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
       }
     }
   }

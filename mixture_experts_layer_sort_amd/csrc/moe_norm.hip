@@ -46,7 +46,7 @@ __device__ __forceinline__ void unpack(const u32x4& v, float (&o)[8]) {
 __device__ __forceinline__ u32x4 pack(const float (&v)[8]) {
   u32x4 o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = f32_to_bf16(v[2 * i]) | (uint32_t)f32_to_bf16(v[2 * i + 1]) << 16;
+  for (int i = 0; i < 4; ++i) o[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
   return o;
 }
 // 8 values at a row (the same for all lanes) and a column of this lane: a scalar base and 32 bits of offset.
@@ -359,8 +359,8 @@ __global__ __launch_bounds__(512) void combine_norm_backward_kernel(NormArgs a) 
     for (int i = 0; i < NC; ++i)
 #pragma unroll
       for (int c = 0; c < 8; ++c) d[i][c] = live[i] ? d[i][c] : 0.f;  // dead lanes: no part of the sums
-    // this wave's parts of the sums over the row (slot k: the shared expert's)
-    auto row = [&](const u32x4 (&v)[NC], int j, float w, uint16_t* to) {
+    // this lane's part of the sum over the row
+    auto row = [&](const u32x4 (&v)[NC], float w, uint16_t* to) {
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -373,13 +373,18 @@ __global__ __launch_bounds__(512) void combine_norm_backward_kernel(NormArgs a) 
         }
         if (to && live[i]) store8(to, col[i], pack(o));
       }
+      return s;
+    };
+    auto add_row = [&](int j, float s) {  // this wave's (slot k: the shared expert's)
       s = sum_lanes<64>(s);
       if (lane == 0) dots[turn][wv][j] = s;
     };
     if constexpr (KR > 0) {
+      float s[KR];  // the exchanges of all rows together, so that none waits for another's
 #pragma unroll
       for (int j = 0; j < KR; ++j) {
-        if (j < a.k) row(y[j], j, scalar(a.w + t * a.k + j), a.d_y ? a.d_y + (t * a.k + j) * a.H : nullptr);
+        s[j] = 0.f;
+        if (j < a.k) s[j] = row(y[j], scalar(a.w + t * a.k + j), a.d_y ? a.d_y + (t * a.k + j) * a.H : nullptr);
         if (j >= PF) {
           load_row(y[j], row_of(next, min(j, a.k - 1)));
         } else {
@@ -387,14 +392,16 @@ __global__ __launch_bounds__(512) void combine_norm_backward_kernel(NormArgs a) 
           for (int i = 0; i < NC; ++i) y[j][i] = z[j][i];
         }
       }
+#pragma unroll
+      for (int j = 0; j < KR; ++j) add_row(j, s[j]);
     } else {
       for (int j = 0; j < a.k; ++j) {
         load_row(y[0], row_of(t, j));
-        row(y[0], j, scalar(a.w + t * a.k + j), a.d_y ? a.d_y + (t * a.k + j) * a.H : nullptr);
+        add_row(j, row(y[0], scalar(a.w + t * a.k + j), a.d_y ? a.d_y + (t * a.k + j) * a.H : nullptr));
       }
     }
     if (a.shared) {
-      row(sh, a.k, gate, a.d_shared ? a.d_shared + t * a.H : nullptr);
+      add_row(a.k, row(sh, gate, a.d_shared ? a.d_shared + t * a.H : nullptr));
       load_row(sh, a.shared + next * a.H);
     }
     __syncthreads();
@@ -415,6 +422,16 @@ __global__ __launch_bounds__(512) void combine_norm_backward_kernel(NormArgs a) 
   for (int i = 0; i < NC; ++i)
     if (live[i]) {
       const int c = col[i] >> 3;
+      if (gridDim.x == 1) {  // these are the sums (and the gradients aligned to 4 bytes only)
+        auto put = [&](float* d, const float4& lo, const float4& hi) {
+          d += col[i];
+          d[0] = lo.x, d[1] = lo.y, d[2] = lo.z, d[3] = lo.w;
+          d[4] = hi.x, d[5] = hi.y, d[6] = hi.z, d[7] = hi.w;
+        };
+        if (a.post) put(a.d_post, dpost[c], dpost[chunks + c]);
+        if (a.next) put(a.d_next, dnext[c], dnext[chunks + c]);
+        continue;
+      }
       if (a.post) to[2 * c] = dpost[c], to[2 * c + 1] = dpost[chunks + c];
       if (a.next) to[a.H / 4 + 2 * c] = dnext[c], to[a.H / 4 + 2 * c + 1] = dnext[chunks + c];
     }
@@ -485,7 +502,7 @@ hipError_t launch_combine_norm_backward(const NormArgs& a, hipStream_t s) {
   const hipError_t e = a.H > 8192  ? launch_backward_rows<4, 0, 0>(a, blocks, s)  // no registers for the rows
                        : a.H > 512 ? launch_backward<2>(a, blocks, s)
                                    : launch_backward<1>(a, blocks, s);
-  if (e != hipSuccess || (!a.post && !a.next)) return e;
+  if (e != hipSuccess || (!a.post && !a.next) || blocks == 1) return e;
   if (a.H <= 2048) launch_weights<16>(a, blocks, s);  // few columns and many parts: 1024 columns of 2048 parts 14 -> 7.4 us
   else launch_weights<64>(a, blocks, s);
   return hipGetLastError();
