@@ -27,11 +27,11 @@
 //
 // Bound by operand movement (LDS reads of both operands once per fragment, direct
 // loads) and, on long runs, by power: 8192 rows of 4096 x 7168 take 167 us on a cool
-// GPU and 196 at the median (2.9 and 2.5 PFLOP/s; matrix instructions alone reach 3.3 to
+// GPU and 196 to 210 at the median (2.9 and 2.3 to 2.5 POP/s; matrix instructions alone reach 3.3 to
 // 3.9 on random bits, a library's 8-bit product 2.0 at this shape), 148 with zeros for
 // operands; without the matrix instructions the rest took 128 us of 133.  256 experts of
-// 7168 x 2048 with 8192 tokens, top-8: gate / up 2160 us, down 1300 (1.7 PFLOP/s: an
-// expert's tiles of 256 rows are two thirds full).  33 rows of 2816 x 4096: 8.6 us, of
+// 7168 x 2048 with 8192 tokens, top-8: gate / up 2160 to 2230 us, down 1300 to 1340 (1.6
+// to 1.7 POP/s: an expert's tiles of 256 rows are two thirds full).  33 rows of 2816 x 4096: 8.6 us, of
 // which the weights' 12 MB are 2.4.
 //
 // At 8192 rows, us, against 176 of that time: four waves of 128 x 128 with accumulators

@@ -36,7 +36,7 @@ struct NormArgs {
 // at once on 256 compute units of 8 waves (16 columns a thread).
 inline int norm_blocks(int T, int H) {
   const int waves = (H + 1023) / 1024, most = 256 * (waves < 8 ? 8 / waves : 1);
-  return T <= 1 ? 1 : T < most ? T : most;
+  return T < most ? T : most;
 }
 inline size_t norm_backward_bytes(int T, int H) {
   const size_t n = (size_t)norm_blocks(T, H) * 2 * H * sizeof(float);

@@ -118,6 +118,22 @@ def test_sizes(T, H, k, form):
     _check(_inputs(T, H, k, *form), T, H, k)
 
 
+@pytest.mark.parametrize("H,k", [(8, 3), (504, 10), (520, 12), (2056, 1), (8192, 8), (8200, 4), (16384, 32)])
+def test_one_token(H, k):
+    """The first launch alone has the norm weights' gradients then; they lie at any 4 bytes and end where they end."""
+    a = _inputs(1, H, k, True, True, True, True, True)
+    _check(a, 1, H, k)
+    ref = _backward(a, 1, H, k, 0.5, 1e-5)
+    b = _buffers(a, 1, H, k)
+    hold = {n: torch.full((H + 5,), 7.0, device=gh.dev()) for n in ("d_post_weight", "d_next_weight")}
+    for n, t in hold.items():
+        b[n] = t[3:H + 3]
+    _backward(a, 1, H, k, 0.5, 1e-5, b)
+    torch.cuda.synchronize()
+    assert all(torch.equal(b[n], ref[n]) for n in ref)
+    assert all((t[:3] == 7).all() and (t[H + 3:] == 7).all() for t in hold.values())
+
+
 @pytest.mark.parametrize("gate,post,nxt,res", [(False, False, True, False), (True, True, True, True), (False, True, False, True)])
 @pytest.mark.parametrize("T,H", [(1, 8), (40, 1024), (6, 7168)])
 def test_without_routed_experts(T, H, gate, post, nxt, res):
