@@ -460,7 +460,8 @@ MOE_API moe_status moe_route_scores(const moe_router* router, int32_t T, const f
  * d_logits_stride apart) from d_topk_w fp32 [T, k] and the picks topk_ids (ids
  * outside [0, E) have no part; an id that a row holds twice counts twice).  The
  * choice itself has no gradient, so bias and groups do not appear.
- * accumulate = 1 adds to d_logits instead of writing it (the losses' part comes
+ * A value is computed in 64 bits and rounded to fp32 once.  accumulate = 1 adds
+ * it, in fp32, to d_logits instead of writing it (the losses' part comes
  * from moe_route_backward with d_topk_w = NULL).  A token with token_mask[t] == 0
  * (u8 [T]; NULL: all count) adds nothing: its row is zero, whatever its inputs
  * hold, or left as it is.  d_logits must not overlap the inputs.  Limits as

@@ -22,8 +22,10 @@
 //
 // Bound by arithmetic: 16384 x 256, sigmoid, 8 groups, top-8: 12.2 us, of which the 64-bit
 // scores are 4, the rounds 1.3, the sort 0.6 and the bytes (17.8 MB) 3.5; one token 3.7.
-// Gradient, bound by memory: 32768 x 256, sigmoid 9.7 us (34 MB written), softmax that is
-// not renormalised 13.4 (67 MB, 5.0 TB/s).
+// Gradient: 32768 x 256, sigmoid 10.5 us (34 MB written), bound by memory; softmax that is
+// not renormalised 16.6 (67 MB, 4.0 TB/s), bound by its 64-bit exponentials: in 32 bits, and
+// the terms rounded before they cancel, it takes 14.1 and loses all digits of a pick whose
+// probability is near 1.
 #include "moe_router.h"
 
 #include "moe_wave.h"
@@ -328,18 +330,13 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouterArgs a)
   }
 }
 
-// exp(x) for x <= 0 to 2^-22: the exponent's whole and broken part in 64 bits (a difference of two logits has no rounding
-// there), the power of the broken part in 32.
-__device__ __forceinline__ float exp_diff(float z, double m) {
-  const double x = ((double)z - m) * 1.4426950408889634074, n = rint(x);
-  const float p = ldexpf(__builtin_amdgcn_exp2f((float)(x - n)), (int)n);
-  return x < -200.0 ? 0.f : p;  // NaN goes on
-}
-
-// Gradient.  L lanes per token; lane j has pick j and its part of the gradient in 64 bits; the parts meet the row's
-// other values in LDS, where a lane has 16 experts in fours (4 (l + L i) .. + 3) or, unaligned, every L-th, so that rows
-// are stored in one run.  DENSE: softmax scores that are not renormalised, which give every expert a gradient; else the
-// logits are read at the picks only, and the rest of a row is zero.
+// Gradient.  L lanes per token; lane j has pick j and its part of the gradient; the picks' values meet the row's others
+// in LDS, where a lane has 16 experts in fours (4 (l + L i) .. + 3) or, unaligned, every L-th, so that rows are stored in
+// one run.  DENSE: softmax scores that are not renormalised, which give every expert a gradient; else the logits are
+// read at the picks only, and the rest of a row is zero.
+// Every value is 64 bits up to one rounding: of a dominant pick g s (1 - s) is left of two terms that cancel, and the
+// parts of an id that a row holds twice may.  So one lane of those with an id has
+// its whole value, which no other adds to.
 template <int L, bool DENSE, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(RouterArgs a) {
   constexpr int TW = 64 / L, N = 16;
@@ -353,7 +350,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
   const bool keep = t < a.T && (!a.mask || a.mask[tt]);
   auto expert = [&](int i) { return VEC ? 4 * (sub + L * (i / 4)) + i % 4 : sub + L * i; };
 
-  float p[N];  // DENSE: logits, then their exponentials
+  float p[N];  // DENSE: logits, then the row's values
   if constexpr (DENSE) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
@@ -378,8 +375,12 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
     if (id >= 0) {
       z = row[id];
       g = (double)a.scale * a.d_w[tt * a.k + sub];
+      mine[id] = __uint_as_float(sub);
     }
   }
+  wave_lds_sync();
+  const bool owner = id >= 0 && __float_as_uint(mine[id]) == (uint32_t)sub;  // one of the lanes that have this id
+  wave_lds_sync();
   float m = id >= 0 ? z : -INFINITY;
   if constexpr (DENSE) {
 #pragma unroll
@@ -398,17 +399,18 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
       ds = e * r * r;
     }
   }
-  double part;
+  double part, rest = 0.0;  // of the pick, and what every expert's score takes off it
   if constexpr (DENSE) {
-    double sum = 0.0;
+    double ex[N], sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) sum += p[i] = exp_diff(p[i], m);
+    for (int i = 0; i < N; ++i) sum += ex[i] = exp64((double)p[i] - m, ex64);
     sum = sum_lanes<L>(sum);
     const double is = sum == 0.0 ? 0.0 : rcp64(sum);
     part = g * s * is;
-    const float f = (float)(-sum_lanes<L>(part) * is);
+    const double f = -sum_lanes<L>(part) * is;
+    rest = s * f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) p[i] *= f;
+    for (int i = 0; i < N; ++i) p[i] = (float)(ex[i] * f);
   } else {
     if (a.renorm) {
       const double sum = sum_lanes<L>(s);
@@ -418,6 +420,15 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
     part = g * ds;
 #pragma unroll
     for (int i = 0; i < N; ++i) p[i] = 0.f;
+  }
+  if (__ballot(id >= 0 && !owner)) {  // an id twice: all of its parts, in the order of the picks
+    double all = 0.0;
+    for (int j = 0; j < a.k; ++j) {
+      const int other = __shfl(id, j, L);
+      const double v = __shfl(part, j, L);
+      all += other == id ? v : 0.0;
+    }
+    part = all;
   }
 
 #pragma unroll
@@ -431,7 +442,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
     }
   }
   wave_lds_sync();
-  if (id >= 0) atomicAdd(&mine[id], (float)part);
+  if (owner) mine[id] = (float)(part + rest);
   wave_lds_sync();
   if (t >= a.T || (a.accumulate && !keep)) return;  // a masked row stays as it is
   float* out = a.d_logits + t * a.ldd;
