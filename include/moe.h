@@ -429,10 +429,12 @@ MOE_API moe_status moe_route_backward(int32_t T, int32_t E, int32_t k, const flo
  * are the top_k largest c of the kept groups' experts in that order (equal ones:
  * the lower id first; -0 == +0), each expert once; weights are
  *   topk_w[t, j] = scale * s_j / (renormalise ? sum of the picks' s : 1)
- * (0 where that sum is 0).  Scores are computed in 64 bits and weights rounded
- * once, so the picks are those of the formulas above.  A row with a NaN (or, for
- * softmax, +inf) gives NaN weights where they depend on it; ids are always in
- * [0, E) and different from each other.
+ * Renormalised weights are the scores' ratios also where the scores are too small
+ * for any number, and 0 where every pick is switched off.  Scores and weights are
+ * computed in 64 bits (within 1e-13) and rounded once, so the picks are those of
+ * the formulas above, unless a score is that near to a border between two fp32
+ * numbers.  A row with a NaN (or, for softmax, +inf) gives NaN weights where they
+ * depend on it; ids are always in [0, E) and different from each other.
  * Supported: 1 <= num_experts <= 1024, 1 <= top_k <= min(num_experts, 32),
  * num_groups a divisor of num_experts, topk_groups groups hold top_k experts,
  * group_top 1 or 2 and no larger than a group; T top_k <= 2^24, row strides at

@@ -67,12 +67,28 @@ __device__ __forceinline__ double rcp64(double d) {
   return fma(r, fma(e, e, e), r);
 }
 
-// 0 below -700, where exp(-l) nears the end of 64 bits.
-__device__ __forceinline__ double sigmoid64(float l, const Exp64& e) {
-  if (l < -700.f) return 0.0;
-  return rcp64(1.0 + exp64(-(double)l, e));
+// A pick's score but for a factor exp(base) that all picks of the token share, and the score's derivative by its logit over
+// the score (softmax: but for the sum's part).
+struct Share {
+  double s, rest;
+};
+// The base of picks whose largest logit is m.  A softmax has it for its sum.  Sigmoids have one where all of them are far
+// below 0: there they are exp(l) (1 + exp(l) is 1 in 64 bits), and renormalised weights, which are ratios, stay those of
+// the formula where exp(l) itself is too small for 64 bits.
+template <bool SOFTMAX>
+__device__ __forceinline__ double share_base(float m) {
+  return m == -INFINITY ? 0.0 : SOFTMAX || m < -40.f ? (double)m : 0.0;
 }
-// The same rounded to 32 bits (0 below -104); l = NaN: unspecified.
+template <bool SOFTMAX>
+__device__ __forceinline__ Share share_of(float l, double base, const Exp64& ex) {
+  const bool plain = SOFTMAX || base != 0.0;
+  const double e = exp64(plain ? (double)l - base : -fabs((double)l), ex);
+  if (plain) return {e, 1.0};
+  const double r = rcp64(1.0 + e);
+  return l < 0.f ? Share{e * r, r} : Share{r, e * r};
+}
+
+// sigmoid(l) rounded to 32 bits (0 below -104); l = NaN: unspecified.
 __device__ __forceinline__ float sigmoid32(float l, const Exp64& e) {
   return (float)rcp64(1.0 + e((double)fminf(fmaxf(-l, -700.f), 700.f)));
 }
@@ -315,14 +331,15 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouterArgs a)
 
   const bool mine = sub < a.k;
   const int id = mine ? from * V + at : 0;
-  double s = 0.0;
-  if (mine) {
-    const float z = row[id];
-    s = SOFTMAX ? exp64((double)z - top, ex64) * inv : sigmoid64(z, ex64);
-  }
+  const float z = mine ? row[id] : -INFINITY;
+  double s;
   if (a.renorm) {
+    s = share_of<SOFTMAX>(z, share_base<SOFTMAX>(max_lanes<L>(z)), ex64).s;
     const double sum = sum_lanes<L>(s);
     s = sum == 0.0 ? 0.0 : s / sum;
+    if (SOFTMAX && inv != inv) s = inv;  // a NaN anywhere in the row
+  } else {
+    s = SOFTMAX ? exp64((double)z - top, ex64) * inv : share_of<false>(z, 0.0, ex64).s;
   }
   if (mine && t < a.T) {
     a.ids[t * a.k + sub] = id;
@@ -389,15 +406,10 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
   m = max_lanes<L>(m);
   if (m == -INFINITY) m = 0.f;
   const Exp64 ex64;
-  double s = 0.0, ds = 0.0;  // score, and its derivative by its own logit (softmax: the first term)
+  Share h = {0.0, 0.0};
   if (id >= 0) {
-    if (a.softmax) {
-      ds = s = exp64((double)z - m, ex64);
-    } else {
-      const double e = exp64(-fabs((double)z), ex64), r = rcp64(1.0 + e);
-      s = z < 0.f ? e * r : r;
-      ds = e * r * r;
-    }
+    if (DENSE || a.softmax) h = share_of<true>(z, m, ex64);  // m: of all experts (DENSE) or of the picks
+    else h = share_of<false>(z, a.renorm ? share_base<false>(m) : 0.0, ex64);
   }
   double part, rest = 0.0;  // of the pick, and what every expert's score takes off it
   if constexpr (DENSE) {
@@ -406,18 +418,18 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
     for (int i = 0; i < N; ++i) sum += ex[i] = exp64((double)p[i] - m, ex64);
     sum = sum_lanes<L>(sum);
     const double is = sum == 0.0 ? 0.0 : rcp64(sum);
-    part = g * s * is;
+    part = g * h.s * is;
     const double f = -sum_lanes<L>(part) * is;
-    rest = s * f;
+    rest = h.s * f;
 #pragma unroll
     for (int i = 0; i < N; ++i) p[i] = (float)(ex[i] * f);
   } else {
     if (a.renorm) {
-      const double sum = sum_lanes<L>(s);
-      const double is = sum == 0.0 ? 0.0 : 1.0 / sum;
-      g = (g - sum_lanes<L>(g * s) * is) * is;
+      const double sum = sum_lanes<L>(h.s);
+      h.s = sum == 0.0 ? 0.0 : h.s / sum;  // the pick's weight
+      g -= sum_lanes<L>(g * h.s);
     }
-    part = g * ds;
+    part = g * h.s * h.rest;
 #pragma unroll
     for (int i = 0; i < N; ++i) p[i] = 0.f;
   }

@@ -13,12 +13,23 @@ def scores(row, kind):
     row = np.asarray(row, np.float64)
     with np.errstate(over="ignore", invalid="ignore"):
         if kind == "sigmoid":
-            return np.array([1.0 / (1.0 + np.exp(-v)) if v >= -700 else 0.0 for v in row])
+            return np.array([1.0 / (1.0 + np.exp(-v)) if v >= 0 else np.exp(v) / (1.0 + np.exp(v)) for v in row])
         m = row.max()
         if m == -np.inf:
             return np.zeros_like(row)
         e = np.exp(row - m)
         return e / e.sum()
+
+
+def shares(z, kind):
+    """Scores of the picks with logits z over their sum, by the scores' logarithms: where the scores themselves leave the
+    64-bit numbers too; 0 where every pick is off."""
+    z = np.asarray(z, np.float64)
+    if not len(z) or z.max() == -np.inf:
+        return np.zeros_like(z)
+    v = -np.logaddexp(0.0, -z) if kind == "sigmoid" else z  # a softmax's sum is the same for all picks
+    e = np.exp(v - v.max())
+    return e / e.sum()
 
 
 def _ranked(values):
@@ -43,10 +54,7 @@ def route(logits, k, kind, bias=None, groups=1, kept=1, top=1, renorm=True, scal
         mine = sorted(_ranked(total)[:kept])
         cand = [e for g in mine for e in range(g * per, (g + 1) * per)]
         ids[t] = [cand[i] for i in _ranked(c[cand])[:k]]
-        v = s[ids[t]]
-        if renorm:
-            v = v / v.sum() if v.sum() != 0.0 else np.zeros_like(v)
-        w[t] = scale * v
+        w[t] = scale * (shares(logits[t, ids[t]], kind) if renorm else s[ids[t]])
     return ids, w
 
 
@@ -61,21 +69,18 @@ def backward(logits, ids, d_w, kind, renorm=True, scale=1.0, mask=None):
         s = scores(logits[t], kind)
         ok = [j for j in range(ids.shape[1]) if 0 <= ids[t, j] < E]
         g = scale * np.asarray(d_w[t], np.float64)
+        v = shares([logits[t, ids[t, j]] for j in ok], kind) if renorm else s[ids[t, ok]]  # in the order of ok
+        dot = adot = 0.0
         if renorm:
-            S = sum(s[ids[t, j]] for j in ok)
-            if S == 0.0:
-                continue
-            dot = sum(g[j] * s[ids[t, j]] for j in ok) / S
-            adot = sum(abs(g[j]) * s[ids[t, j]] for j in ok) / S
-            gm, g = (np.abs(g) + adot) / S, (g - dot) / S
-        else:
-            gm = np.abs(g)
-        for j in ok:
+            dot = sum(g[j] * v[i] for i, j in enumerate(ok))
+            adot = sum(abs(g[j]) * v[i] for i, j in enumerate(ok))
+        for i, j in enumerate(ok):
             e = ids[t, j]
             z = float(logits[t, e])
-            ds = np.exp(-abs(z)) / (1.0 + np.exp(-abs(z))) ** 2 if kind == "sigmoid" else s[e]
-            d[t, e] += g[j] * ds
-            mag[t, e] += gm[j] * ds
+            # of the weight by its own logit, but for the sum's part
+            dv = v[i] if kind == "softmax" else v[i] * (1.0 / (1.0 + np.exp(z)) if z < 0 else np.exp(-z) / (1.0 + np.exp(-z)))
+            d[t, e] += (g[j] - dot) * dv
+            mag[t, e] += (abs(g[j]) + adot) * dv
         if kind == "softmax" and not renorm:
             dot = sum(g[j] * s[ids[t, j]] for j in ok)
             d[t] -= s * dot
