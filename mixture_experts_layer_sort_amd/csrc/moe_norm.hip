@@ -110,7 +110,8 @@ __device__ __forceinline__ void add_rows(const NormArgs& a, size_t t, int j, con
     }
 }
 
-// Columns of this thread: chunks of 8, a block's width apart; past the row's end the last chunk again (`live`: not).
+// Columns of this thread: chunks of 8, a block's width apart; past the row's end the last chunk again (`live`: not).  Sums
+// leave those out whole: with factors of zero an infinity in the last chunk would give them a NaN.
 template <int NC>
 __device__ __forceinline__ void columns(int H, uint32_t (&col)[NC], bool (&live)[NC]) {
 #pragma unroll
@@ -281,12 +282,14 @@ __global__ __launch_bounds__(512) void combine_norm_backward_kernel(NormArgs a) 
         unpack(vo[i], r);
         unpack(vn[i], n);
         unpack(weight(a.next, gnext, i), g);
+        float u0 = s[0], u1 = s[1];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const float rl = live[i] ? r[c] : 0.f;
-          s[0] = fmaf(rl, rl, s[0]);
-          s[1] = fmaf(n[c] * g[c], rl, s[1]);
+          u0 = fmaf(r[c], r[c], u0);
+          u1 = fmaf(n[c] * g[c], r[c], u1);
         }
+        s[0] = live[i] ? u0 : s[0];
+        s[1] = live[i] ? u1 : s[1];
       }
       block_sum<2>(s, part[0], waves);
       const float q = 1.f / sqrtf(s[0] * rH + a.eps), f = q * q * (s[1] * rH);
@@ -339,12 +342,14 @@ __global__ __launch_bounds__(512) void combine_norm_backward_kernel(NormArgs a) 
       for (int i = 0; i < NC; ++i) {
         float g[8];
         unpack(weight(a.post, gpost, i), g);
+        float u0 = s[0], u1 = s[1];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          m[i][c] = live[i] ? m[i][c] : 0.f;
-          s[0] = fmaf(m[i][c], m[i][c], s[0]);
-          s[1] = fmaf(d[i][c] * g[c], m[i][c], s[1]);
+          u0 = fmaf(m[i][c], m[i][c], u0);
+          u1 = fmaf(d[i][c] * g[c], m[i][c], u1);
         }
+        s[0] = live[i] ? u0 : s[0];
+        s[1] = live[i] ? u1 : s[1];
       }
       block_sum<2>(s, part[1], waves);
       const float q = 1.f / sqrtf(s[0] * rH + a.eps), f = q * q * (s[1] * rH);
@@ -360,10 +365,6 @@ __global__ __launch_bounds__(512) void combine_norm_backward_kernel(NormArgs a) 
         add_to(dpost, i, p);
       }
     }
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-#pragma unroll
-      for (int c = 0; c < 8; ++c) d[i][c] = live[i] ? d[i][c] : 0.f;  // dead lanes: no part of the sums
     // this lane's part of the sum over the row
     auto row = [&](const u32x4 (&v)[NC], float w, uint16_t* to) {
       float s = 0.f;
@@ -371,11 +372,13 @@ __global__ __launch_bounds__(512) void combine_norm_backward_kernel(NormArgs a) 
       for (int i = 0; i < NC; ++i) {
         float x[8], o[8];
         unpack(v[i], x);
+        float u = s;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          s = fmaf(d[i][c], x[c], s);
+          u = fmaf(d[i][c], x[c], u);
           o[c] = w * d[i][c];
         }
+        s = live[i] ? u : s;
         if (to && live[i]) store8(to, col[i], pack(o));
       }
       return s;
