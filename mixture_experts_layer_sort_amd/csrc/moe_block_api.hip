@@ -1,6 +1,8 @@
 // C ABI entry points of the scored routing and of the end of an expert block,
 // with their gradients: host-side argument checks, then launches on the caller's
 // stream.  Nothing here allocates device memory, synchronises or reads device data.
+#include <cmath>
+
 #include "../../include/moe.h"
 #include "moe_norm.h"
 #include "moe_router.h"
@@ -15,7 +17,6 @@ template <class... P>
 bool aligned_to(size_t n, const P*... p) {  // null is
   return (aligned(p, n) && ...);
 }
-bool finite(float v) { return v >= -3.0e38f && v <= 3.0e38f; }
 
 moe_status check_router(const moe_router* r, int32_t T) {
   if (!r || T < 0) return MOE_ERR_INVALID_ARG;
@@ -27,7 +28,7 @@ moe_status check_router(const moe_router* r, int32_t T) {
   if (r->group_top != 1 && r->group_top != 2) return MOE_ERR_UNSUPPORTED;
   if (r->group_top > E / G) return MOE_ERR_UNSUPPORTED;
   if (r->renormalise != 0 && r->renormalise != 1) return MOE_ERR_INVALID_ARG;
-  if (!finite(r->scale)) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(r->scale)) return MOE_ERR_INVALID_ARG;
   return (long long)T * k > (1LL << 24) ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
@@ -93,7 +94,7 @@ moe_status moe_combine_norm(int32_t T, int32_t H, int32_t k, const uint16_t* y, 
                             uint16_t* out, uint16_t* normed, hipStream_t stream) {
   const moe_status st = check_norm(T, H, k);
   if (st != MOE_OK) return st;
-  if (!(eps >= 0.f && finite(eps)) || !finite(scale)) return MOE_ERR_INVALID_ARG;
+  if (!(eps >= 0.f && std::isfinite(eps)) || !std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if ((k > 0) != (y != nullptr) || (k > 0) != (topk_w != nullptr)) return MOE_ERR_INVALID_ARG;
   if (!out || (k == 0 && !shared) || (shared_gate && !shared)) return MOE_ERR_INVALID_ARG;
@@ -122,7 +123,7 @@ moe_status moe_combine_norm_backward(int32_t T, int32_t H, int32_t k, const uint
                                      hipStream_t stream) {
   const moe_status st = check_norm(T, H, k);
   if (st != MOE_OK) return st;
-  if (!(eps >= 0.f && finite(eps)) || !finite(scale)) return MOE_ERR_INVALID_ARG;
+  if (!(eps >= 0.f && std::isfinite(eps)) || !std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if ((k > 0) != (y != nullptr) || (k > 0) != (topk_w != nullptr)) return MOE_ERR_INVALID_ARG;
   if ((k == 0 && !shared) || (shared_gate && !shared)) return MOE_ERR_INVALID_ARG;
