@@ -356,12 +356,15 @@ hipError_t launch_grouped(const Int8Args& a, int cus, hipStream_t s) {
 // behind a launch of 3.5; 8 rows 6.0 behind it).
 bool int8_decode_fits(int M, int K) { return M <= 16 && M * (int8_pad(K) / 128) <= 224; }
 
-// Grouped: while every block has one item (3 blocks a compute unit), since a second item's rows are quantised with no
-// weights on their way beside it (H 7168, I 2048, 256 experts, top-8: gate / up of one token 46.6 us against 42.3 and the
-// quantiser's launch of 4.6, of two, in 1.3 rounds, 101 against 80.7; H 4096, I 1408, 64 experts, top-6, one token 20.4
-// against 21.7 and 3.8); while an expert's rows are little work (gate / up of H 4096 and 2 experts of I 1024, 8 tokens 13.5
-// against 12.6 and 2.7, 14 tokens 20.4 against 12.6 and 3.0; one of I 4096, 9 tokens 23.8 against 12.6 and 8.0); and while
-// two blocks' codes fit a CU's LDS.  0: codes.
+// Grouped: up to 3 items a compute unit.  Blocks that quantise run two at a time there (211 registers), those that read
+// codes three, so past 2 items the first have a second round, whose rows are quantised with no weights on their way beside
+// it; the launch for the codes costs about as much (us, quantising against codes and their launch: gate / up of H 7168, I
+// 2048, one token, top-8, 512 items 46.6 and 42.3 + 4.6, top-9, 576 items 62.3 and 56.1 + 4.7, top-12, 768 items 67.3 and
+// 61.1 + 4.8, two tokens, 1024 items 101 and 80.7; of H 4096, I 1408, top-6, two tokens, 528 items 33.3 and 30.3 + 4.7;
+// down of the first, top-6, 672 items 21.9 and 18.2 + 4.7, of the second, 768 items 17.7 and 13.9 + 4.7).  While an
+// expert's rows are little work (gate / up of H 4096 and 2 experts of I 1024, 8 tokens 13.5 against 12.6 and 2.7, 14 tokens
+// 20.4 against 12.6 and 3.0; one of I 4096, 9 tokens 23.8 against 12.6 and 8.0).  And while the codes take 64 KB (two
+// blocks' fit a CU's LDS up to 59, beside the sums and offsets).  0: codes.
 int int8_block_rows(Int8Mode mode, const Int8Args& a, int T, int cus) {
   const int cap = min(T, 16), rows = min(cap, a.rows / a.E + 1);
   const bool little = rows * (int8_pad(a.K) / 128) < 200;
