@@ -13,14 +13,17 @@
 //   dm = post ? q1 (c - m q1^2 <c m>) : b
 //   d_y_j = w_j dm,  d_w_j = sum dm y_j,  d_shared = gate dm,  d_gate = sum dm shared
 //
-// Both are bound by memory: every row is read once and written once, with stores
+// Both are bound by memory: every row is read once and written once (gradients of more
+// than 10 rows or more than 8192 columns with a norm of the sum: twice), with stores
 // that do not stay in the caches (non-temporal: forward 262 -> 242 us at 8192 x
 // 7168, top-8).  A block takes a token, a thread 8 NC columns of it in registers, so
 // that a row's norm needs one exchange over the block and no second read.
 //
-// Gradients: the token's k rows stay in registers from the sum to its gradient, a
-// register that is done with takes a row of the next token, and PF rows of it have
-// registers of their own, so that loads are in flight through every exchange.
+// Gradients: up to 10 rows of up to 8192 columns stay in registers from the sum to its
+// gradient, a register that is done with takes a row of the next token, and PF rows of
+// it have registers of their own, so that loads are in flight through every exchange.
+// Beyond that there are no registers for them: rows are loaded one by one, with a norm
+// of the sum twice.
 // Nothing else may wait for vector loads in between: the norms' weights are in LDS,
 // the rows' weights go through the scalar cache (as vector loads they cost 600 us
 // against 493).  The norm weights' gradients are sums over tokens: a block adds those
@@ -34,7 +37,9 @@
 //
 // Measured, with a gated shared expert and both norms: 8192 x 7168, top-8: forward
 // 242 us (1.41 GB, 5.8 TB/s), gradients 489 + 5 us (2.58 GB, 5.3 TB/s; a large copy
-// reaches 5.2); 8192 x 4096, top-6 without a shared expert: gradients 207 + 5 us.
+// reaches 5.2); 8192 x 4096, top-6 without a shared expert: gradients 207 + 5 us.  Rows
+// loaded one by one: 4096 x 4096, top-16 231 us without a norm of the sum (1.28 GB, 5.5
+// TB/s) and 291 with it, 4096 x 12288, top-8 411 (2.2 GB, 5.4 TB/s) and 497.
 #include "moe_norm.h"
 
 #include "moe_device.h"

@@ -8,7 +8,8 @@
 //
 // Which of two experts is picked can hang on the last bit of a score, so scores
 // are computed in 64 bits (relative error below 3e-14) and rounded once to the
-// 32 bits that the definition names: picks are the same whatever computes them.
+// 32 bits that the definition names: picks are the same whatever computes them (unless
+// a score is that near to a border between two 32-bit numbers).
 // (On this GPU a 64-bit multiply-add issues like a 32-bit one.)
 //
 // A token has L lanes, a lane V consecutive experts, so that positions order
@@ -22,8 +23,10 @@
 //
 // Bound by arithmetic: 16384 x 256, sigmoid, 8 groups, top-8: 12.2 us, of which the 64-bit
 // scores are 4, the rounds 1.3, the sort 0.6 and the bytes (17.8 MB) 3.5; one token 3.7.
+// Softmax without groups: 16384 x 64 5.9 us, x 128 7.5, x 256 11.3, x 384 and x 512 (64
+// lanes a token) 23; one token of 1024 experts 5.4.
 // Gradient: 32768 x 256, sigmoid 10.5 us (34 MB written), bound by memory; softmax that is
-// not renormalised 16.6 (67 MB, 4.0 TB/s), bound by its 64-bit exponentials: in 32 bits, and
+// not renormalised 16.1 (67 MB, 4.2 TB/s), bound by its 64-bit exponentials: in 32 bits, and
 // the terms rounded before they cancel, it takes 14.1 and loses all digits of a pick whose
 // probability is near 1.
 #include "moe_router.h"
